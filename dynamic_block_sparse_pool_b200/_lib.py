@@ -39,6 +39,15 @@ SIGNATURES = {
     "dsa_hilbert_order": (_i, [_i, _i, _i, _i, _vp]),
     "dsa_gilbert_order": (_i, [_i, _i, _i, _i, _vp]),
     "dsa_permute_tokens": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
+    "dsa_rope_table": (_i, [_i, _i, _f, _vp]),
+    "dsa_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _f, _vp, _vp,
+                              _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dsa_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp,
+                                  _vp, _f, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                  _vp]),
+    "dsa_qk_norm_rope_bwd_workspace_size": (_sz, [_i]),
+    "dsa_pack8": (_i, [_vp, _i, _sz, _i, _vp, _vp, _vp]),
+    "dsa_unpack8": (_i, [_vp, _vp, _i, _sz, _i, _vp, _vp]),
     "dsa_select_topp_static": (_i, [_vp, _i, _i, _f, _vp, _vp, _vp, _vp, _vp]),
     "dsa_selftest_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
     "dsa_selftest_exp2_poly": (_i, [_vp, _vp, _i, _vp]),

@@ -16,6 +16,8 @@ enum : unsigned {
   kErrAlign = 16u,       // dynamic shared memory not 1024-byte aligned
   kErrPerm = 32u,        // a token permutation entry outside [0, N)
   kErrRowOrder = 64u,    // an attention row-order entry outside [0, rows)
+  kErrPosition = 128u,   // a rotation position past the end of its axis' table
+  kErrLength = 256u,     // a cached length outside [0, capacity]
 };
 
 // Upper bound for one mbarrier wait before a kernel gives up (nanoseconds).
@@ -93,6 +95,11 @@ cudaError_t launch_attn_bwd_sm100(const void* q, const void* k, const void* v, c
 // One CTA that waits on an mbarrier nobody arrives at, with the given limit.
 cudaError_t launch_wait_timeout(unsigned long long limit_ns, unsigned* err, cudaStream_t s);
 cudaError_t launch_exp2_poly(const float* x, float* y, int n, cudaStream_t s);
+// Rows of D values as int8 codes with one fp32 scale each, and back.
+cudaError_t launch_pack8(const void* x, bool bf16, long long rows, int D, int8_t* codes,
+                         float* scales, cudaStream_t s);
+cudaError_t launch_unpack8(const int8_t* codes, const float* scales, bool bf16, long long rows,
+                           int D, void* x, cudaStream_t s);
 cudaError_t launch_block_mass(const float* lse, const float* blk_lse, int BH, int N,
                               int block, const int32_t* row_ptr, float* mass,
                               cudaStream_t s);

@@ -657,14 +657,16 @@ dsa_status dsa_device_status(void* stream) {
   const unsigned zero = 0;
   e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
   if (e != cudaSuccess) return cuda_fail(e, "clear device error word");
-  return fail(DSA_ERR_DEVICE, "device error word 0x%x:%s%s%s%s%s%s%s", word,
+  return fail(DSA_ERR_DEVICE, "device error word 0x%x:%s%s%s%s%s%s%s%s%s", word,
               (word & dsa::kErrCsrIndex) ? " csr-index-out-of-range" : "",
               (word & dsa::kErrRowPtr) ? " bad-row-ptr" : "",
               (word & dsa::kErrProb) ? " probability-outside-[0,1]" : "",
               (word & dsa::kErrTimeout) ? " wait-timeout" : "",
               (word & dsa::kErrAlign) ? " shared-memory-misaligned" : "",
               (word & dsa::kErrPerm) ? " permutation-index-out-of-range" : "",
-              (word & dsa::kErrRowOrder) ? " row-order-index-out-of-range" : "");
+              (word & dsa::kErrRowOrder) ? " row-order-index-out-of-range" : "",
+              (word & dsa::kErrPosition) ? " rotation-position-out-of-range" : "",
+              (word & dsa::kErrLength) ? " cached-length-out-of-range" : "");
 }
 
 }  // extern "C"

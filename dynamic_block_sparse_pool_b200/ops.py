@@ -298,6 +298,255 @@ class HilbertOrder:
         return permute_tokens(x, self.perm, True, out)
 
 
+# ------------------------------------------------- around the attention --
+
+class Act8(NamedTuple):
+    """Activation rows of D values in 8 bits: the value held is code * scale."""
+
+    codes: torch.Tensor        # int8 [..., D]
+    scales: torch.Tensor       # fp32 [...]
+
+
+def _check_act8(a: Act8) -> None:
+    c, s = a
+    if c.dtype != torch.int8 or s.dtype != torch.float32 or not c.is_cuda or s.device != c.device:
+        raise ValueError("8-bit rows are int8 codes and fp32 scales on one CUDA device")
+    if not c.is_contiguous() or not s.is_contiguous() or c.shape[:-1] != s.shape:
+        raise ValueError("codes [..., D] and scales [...] must be contiguous and match")
+
+
+def pack8(x: torch.Tensor) -> Act8:
+    """The rows of x [..., D] (contiguous, bf16 or fp32) in 8 bits: one scale
+    amax / 127 for each row, half-even rounding."""
+    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
+        raise ValueError("x must be a contiguous CUDA tensor [..., D]")
+    dt, D = _dtype_code(x), x.shape[-1]
+    a = Act8(torch.empty(x.shape, device=x.device, dtype=torch.int8),
+             torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32))
+    if x.numel() == 0:
+        return a
+    with torch.cuda.device(x.device):
+        st = lib().dsa_pack8(x.data_ptr(), dt, x.numel() // D, D, a.codes.data_ptr(),
+                             a.scales.data_ptr(), _stream(x))
+    check(st, "dsa_pack8")
+    return a
+
+
+def unpack8(a: Act8, dtype: torch.dtype = torch.bfloat16,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that 8-bit rows stand for, as bf16 or fp32."""
+    _check_act8(a)
+    if out is None:
+        out = torch.empty(a.codes.shape, device=a.codes.device, dtype=dtype)
+    elif out.shape != a.codes.shape or out.device != a.codes.device or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of the codes' shape and device")
+    dt, D = _dtype_code(out), out.shape[-1]
+    if out.numel() == 0:
+        return out
+    with torch.cuda.device(out.device):
+        st = lib().dsa_unpack8(a.codes.data_ptr(), a.scales.data_ptr(), dt, out.numel() // D, D,
+                               out.data_ptr(), _stream(out))
+    check(st, "dsa_unpack8")
+    return out
+
+
+def rope_table(positions: int, pairs: int, theta: float = 10000.0) -> torch.Tensor:
+    """Host fp32 [positions, pairs, 2]: cos and sin of p * theta^(-i / pairs)."""
+    if positions < 1 or pairs < 1:
+        raise ValueError("positions and pairs must be at least 1")
+    t = torch.empty(positions, pairs, 2, dtype=torch.float32)
+    check(lib().dsa_rope_table(positions, pairs, float(theta), t.data_ptr()), "dsa_rope_table")
+    return t
+
+
+class RopePlan:
+    """Positions and rotation tables of the tokens of one layout, on the device.
+
+    pos     [N, axes] or [B, N, axes] integers, up to three axes (a grid's
+            t, y, x, or one axis of plain positions); below 0: the axis'
+            pairs of that token do not turn.
+    pairs   rotated pairs of each axis, in the order of the pairs of a row;
+            at most D/2 in all, the rest do not turn.
+    theta   base of the frequencies, one for all axes or one for each.
+    halves  False: pair m is elements (2m, 2m+1); True: (m, m + D/2).
+    lengths positions that each axis' table covers (default: those in pos)."""
+
+    def __init__(self, pos: torch.Tensor, pairs, theta=10000.0, halves: bool = False,
+                 lengths=None, device=None):
+        pairs = [int(p) for p in pairs]
+        if not 1 <= len(pairs) <= 3 or min(pairs) < 0 or max(pairs) < 1:
+            raise ValueError("pairs: one to three axes, at least one of them with a pair")
+        thetas = list(theta) if isinstance(theta, (tuple, list)) else [theta] * len(pairs)
+        if len(thetas) != len(pairs) or (lengths is not None and len(lengths) != len(pairs)):
+            raise ValueError("theta and lengths must match the axes of pairs")
+        dev = device if device is not None else pos.device if pos.is_cuda else \
+            torch.device("cuda", torch.cuda.current_device())
+        if lengths is None:
+            flat = pos.reshape(-1, pos.shape[-1])
+            top = flat.amax(0).tolist() if flat.numel() else [0] * flat.shape[-1]
+            lengths = [max(int(t), 0) + 1 for t in top[:len(pairs)]]
+            lengths += [1] * (len(pairs) - len(lengths))
+        self.pairs = tuple(pairs + [0] * (3 - len(pairs)))
+        self.lengths = tuple([int(n) for n in lengths] + [1] * (3 - len(pairs)))
+        self.halves = bool(halves)
+        self.table = torch.cat([rope_table(n, p, t).reshape(-1, 2) for n, p, t in
+                                zip(self.lengths, pairs, thetas) if p]).to(dev)
+        self._axes = torch.tensor(self.pairs + self.lengths, dtype=torch.int32)
+        self.pos = self._positions(pos, dev)
+
+    @staticmethod
+    def _positions(pos: torch.Tensor, dev) -> torch.Tensor:
+        if pos.dim() not in (2, 3) or not 1 <= pos.shape[-1] <= 3 or pos.is_floating_point():
+            raise ValueError("pos must be integers [N, axes] or [B, N, axes], up to three axes")
+        pos = pos.to(device=dev, dtype=torch.int32)
+        if pos.shape[-1] < 3:
+            pos = torch.nn.functional.pad(pos, (0, 3 - pos.shape[-1]), value=-1)
+        return (pos if pos.dim() == 3 else pos[None]).contiguous()
+
+    @classmethod
+    def grid(cls, T: int, H: int, W: int, head_dim: int, n_prefix: int = 0, pairs=None,
+             theta=10000.0, halves: bool = False, order: Optional[torch.Tensor] = None, t0: int = 0,
+             device=None) -> "RopePlan":
+        """The tokens of a T x H x W grid in row-major (t, y, x) order, behind
+        n_prefix text tokens that do not turn; `order` (hilbert_order's or
+        gilbert_order's perm) lists them in that order instead, t0 is the
+        first frame's position.  By default the axes share the D/2 pairs
+        evenly, the t axis taking what is left over."""
+        if pairs is None:
+            third = head_dim // 2 // 3
+            pairs = (head_dim // 2 - 2 * third, third, third)
+        t, y, x = torch.meshgrid(torch.arange(T), torch.arange(H), torch.arange(W), indexing="ij")
+        pos = torch.full((n_prefix + T * H * W, 3), -1, dtype=torch.int32)
+        pos[n_prefix:] = torch.stack([t.reshape(-1) + t0, y.reshape(-1), x.reshape(-1)], 1).int()
+        if order is not None:
+            pos = pos[order.cpu().long()]
+        return cls(pos, pairs, theta, halves, device=device)
+
+    def at(self, pos: torch.Tensor) -> "RopePlan":
+        """The same tables for other tokens: pos as in the constructor, within
+        the tables' lengths (a position past them is reported by
+        device_status and does not turn)."""
+        new = object.__new__(RopePlan)
+        new.__dict__.update(self.__dict__)
+        new.pos = self._positions(pos, self.table.device)
+        return new
+
+
+def _token_rows(x: torch.Tensor, what: str):
+    """Strides of b, n, h of token-major rows [B, N, H, D], D contiguous."""
+    if x.dim() != 4 or not x.is_cuda or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError(f"{what} must be a CUDA tensor [B, N, H, D] with contiguous rows")
+    return [x.stride(i) if x.shape[i] > 1 else 0 for i in range(3)]
+
+
+def _strides6(a, b) -> torch.Tensor:
+    return torch.tensor(a + b, dtype=torch.int64)
+
+
+def _check_norm_rope(xq, xk, wq, wk, plan: RopePlan):
+    """(q data, k data, q scales, k scales, B, N, Hq, Hk, D) of either kind of x."""
+    if isinstance(xq, Act8) != isinstance(xk, Act8):
+        raise ValueError("xq and xk must both be tensors or both be 8-bit rows")
+    sq = sk = None
+    if isinstance(xq, Act8):
+        _check_act8(xq)
+        _check_act8(xk)
+        (xq, sq), (xk, sk) = xq, xk
+    if xq.dim() != 4 or xk.dim() != 4 or xq.dtype != xk.dtype or xq.device != xk.device:
+        raise ValueError("xq and xk must be [B, N, H, D] of one dtype on one device")
+    B, N, Hq, D = xq.shape
+    if xk.shape[0] != B or xk.shape[1] != N or xk.shape[3] != D:
+        raise ValueError("xq and xk must share B, N and D")
+    for w in (wq, wk):
+        if w is not None and (w.dtype != torch.float32 or w.device != xq.device or w.numel() != D
+                              or not w.is_contiguous()):
+            raise ValueError("weights must be contiguous fp32 [D] on x's device")
+    if plan.pos.device != xq.device or plan.pos.shape[1] != N or plan.pos.shape[0] not in (1, B):
+        raise ValueError(f"the plan's positions {tuple(plan.pos.shape)} do not fit B = {B}, N = {N} on x's device")
+    return xq, xk, sq, sk, B, N, Hq, xk.shape[2], D
+
+
+def qk_norm_rope(xq, xk, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], plan: RopePlan,
+                 eps: float = 1e-6, save8: bool = False, dtype: torch.dtype = torch.bfloat16):
+    """(q, k) [B, H, N, D]: each head's row of xq, xk [B, N, H, D] normalised
+    by its root mean square, times wq or wk [D] (fp32, None: ones), turned by
+    its token's position.
+
+    xq and xk may be strided views (the fused projection's output), or Act8
+    rows that an earlier call saved (q and k then come in `dtype`).  save8:
+    also returns the rows of xq and xk in 8 bits, (q, k, xq8, xk8)."""
+    dx, dk, sq, sk, B, N, Hq, Hk, D = _check_norm_rope(xq, xk, wq, wk, plan)
+    from8 = sq is not None
+    if save8 and from8:
+        raise ValueError("save8: xq and xk already are 8-bit rows")
+    dt = dtype if from8 else dx.dtype
+    q = torch.empty(B, Hq, N, D, device=dx.device, dtype=dt)
+    k = torch.empty(B, Hk, N, D, device=dx.device, dtype=dt)
+    code = _dtype_code(q)
+    st6 = _strides6(_token_rows(dx, "xq"), _token_rows(dk, "xk"))
+    q8 = k8 = Act8(None, None)
+    if save8:
+        q8, k8 = (Act8(torch.empty(B, N, h, D, device=dx.device, dtype=torch.int8),
+                       torch.empty(B, N, h, device=dx.device, dtype=torch.float32)) for h in (Hq, Hk))
+    if B * N > 0:
+        with torch.cuda.device(dx.device):
+            st = lib().dsa_qk_norm_rope(
+                dx.data_ptr(), dk.data_ptr(), _ptr(sq), _ptr(sk), st6.data_ptr(), code, B, N, Hq, Hk, D,
+                _ptr(wq), _ptr(wk), float(eps), plan.table.data_ptr(), plan.pos.data_ptr(),
+                1 if plan.pos.shape[0] > 1 else 0, plan._axes.data_ptr(), int(plan.halves), q.data_ptr(),
+                k.data_ptr(), _ptr(q8.codes), _ptr(q8.scales), _ptr(k8.codes), _ptr(k8.scales),
+                _stream(dx))
+        check(st, "dsa_qk_norm_rope")
+    return (q, k, q8, k8) if save8 else (q, k)
+
+
+def qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, xq, xk, wq: Optional[torch.Tensor],
+                     wk: Optional[torch.Tensor], plan: RopePlan, eps: float = 1e-6,
+                     dxq: Optional[torch.Tensor] = None, dxk: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """(dxq, dxk [B, N, H, D], dwq, dwk fp32 [D]): qk_norm_rope's gradients for
+    dq, dk [B, H, N, D].  xq, xk as the forward took them, or the Act8 rows it
+    saved.  dxq and dxk may be given, strided views of a fused buffer among
+    them."""
+    vq, vk, sq, sk, B, N, Hq, Hk, D = _check_norm_rope(xq, xk, wq, wk, plan)
+    for g, h in ((dq, Hq), (dk, Hk)):
+        if tuple(g.shape) != (B, h, N, D) or not g.is_contiguous() or g.device != vq.device or \
+                g.dtype != dq.dtype:
+            raise ValueError("dq and dk must be contiguous [B, H, N, D] of one dtype on x's device")
+    if sq is None and vq.dtype != dq.dtype:
+        raise ValueError("dq and dk must have x's dtype")
+    code = _dtype_code(dq)
+    outs = []
+    for d, h in ((dxq, Hq), (dxk, Hk)):
+        if d is None:
+            d = torch.empty(B, N, h, D, device=dq.device, dtype=dq.dtype)
+        elif tuple(d.shape) != (B, N, h, D) or d.dtype != dq.dtype or d.device != dq.device:
+            raise ValueError("dxq and dxk must be [B, N, H, D] of dq's dtype and device")
+        elif any(d.shape[i] > 1 and d.stride(i) == 0 for i in range(3)):
+            raise ValueError("rows of dxq and dxk must not overlap")
+        outs.append(d)
+    dxq, dxk = outs
+    st6 = _strides6(_token_rows(vq, "xq"), _token_rows(vk, "xk"))
+    dst6 = _strides6(_token_rows(dxq, "dxq"), _token_rows(dxk, "dxk"))
+    dwq = torch.empty(D, device=dq.device, dtype=torch.float32)
+    dwk = torch.empty(D, device=dq.device, dtype=torch.float32)
+    if B * N == 0:
+        return dxq, dxk, dwq.zero_(), dwk.zero_()
+    if workspace is None:
+        workspace = torch.empty(int(lib().dsa_qk_norm_rope_bwd_workspace_size(D)), device=dq.device,
+                                dtype=torch.uint8)
+    with torch.cuda.device(dq.device):
+        st = lib().dsa_qk_norm_rope_bwd(
+            dq.data_ptr(), dk.data_ptr(), vq.data_ptr(), vk.data_ptr(), _ptr(sq), _ptr(sk), st6.data_ptr(),
+            code, B, N, Hq, Hk, D, _ptr(wq), _ptr(wk), float(eps), plan.table.data_ptr(),
+            plan.pos.data_ptr(), 1 if plan.pos.shape[0] > 1 else 0, plan._axes.data_ptr(),
+            int(plan.halves), dxq.data_ptr(), dxk.data_ptr(), dst6.data_ptr(), dwq.data_ptr(),
+            dwk.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream(dq))
+    check(st, "dsa_qk_norm_rope_bwd")
+    return dxq, dxk, dwq, dwk
+
+
 def selftest_wait_timeout(limit_ns: int = 1_000_000, device: Optional[torch.device] = None) -> None:
     """Launch the failure-detection self-test: a bounded wait that runs out
     after limit_ns and records a wait timeout (dsa_device_status then raises)."""

@@ -21,6 +21,15 @@
  *                    exact attention weights (the next mask of a schedule).
  *   dsa_sparse_attention_host  the four calls above on host-resident Q, K, V
  *                    (chunks of heads, copies overlapped with compute).
+ *   dsa_qk_norm_rope, dsa_qk_norm_rope_bwd  the step before the attention:
+ *                    per-head norms of queries and keys with the position
+ *                    rotation, token-major in, head-major out; its gradient.
+ *   dsa_window_attn_fwd, dsa_window_attn_bwd, dsa_window_attn_decode  the
+ *                    fixed mask beside the dynamic ones: a local window with
+ *                    first tokens that stay visible, its gradient, and its
+ *                    form for a few new tokens over a cache.
+ *   dsa_pack8, dsa_unpack8  activations kept in 8 bits between the forward
+ *                    and the backward.
  *   dsa_selftest_wait_timeout, dsa_selftest_exp2_poly  self-tests.
  *   dsa_hilbert_order, dsa_gilbert_order, dsa_permute_tokens  token
  *                    reordering along a 3-D Hilbert curve (the enclosing
@@ -427,6 +436,113 @@ dsa_status dsa_gilbert_order(int T, int H, int W, int n_prefix, int32_t* perm);
  */
 dsa_status dsa_permute_tokens(const void* src, void* dst, dsa_dtype dt, int B, int H, int N, int D,
                               const int32_t* perm, int inverse, void* stream);
+
+/*
+ * The (cos, sin) table of one rotation axis (host function, no device work):
+ *   table[(p * pairs + i) * 2 + {0, 1}] = cos, sin of p * theta^(-i / pairs)
+ * for p = 0 .. positions-1, i = 0 .. pairs-1, computed in 64 bits (a position
+ * of 100,000 turns its fastest pair 15,900 times; an fp32 angle would keep
+ * two digits of the turn) and rounded to fp32.
+ * The table of dsa_qk_norm_rope is the axes' tables one after another.
+ *   table  host out, fp32 [positions][pairs][2].
+ * Errors: DSA_ERR_INVALID_ARG for a null table, positions < 1, pairs outside
+ * 1..64, theta not finite or <= 0, or positions * pairs above 2^30.
+ */
+dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table);
+
+/*
+ * Per-head norms of queries and keys with the position rotation, one pass
+ * from the projection's layout to the attention's.  (No counterpart in the
+ * papers: the video DiTs they measure normalise and rotate q and k right
+ * before the attention they speed up.)
+ *
+ * For every row x of D values (one token and head), r = 1 / sqrt(mean(x^2) +
+ * eps):  n = x * r * w;  pair m of the D/2 pairs of n -- elements (2m, 2m+1),
+ * or with `halves` (m, m + D/2) -- turns by its angle:
+ *   (a, b) -> (a cos - b sin, a sin + b cos).
+ * Pairs 0 .. pairs[0]-1 belong to axis 0 (t), the next pairs[1] to axis 1 (y),
+ * the next pairs[2] to axis 2 (x), the rest do not turn.  Pair i of axis a at
+ * position p turns by entry (p, i) of the axis' table.
+ *
+ *   xq, xk     [B, N, Hq or Hk, D] in dt, read through `x_strides` (D
+ *              contiguous); 16-byte aligned, strides multiples of 16 bytes.
+ *   x_strides  host, int64 [6]: xq's strides of b, n, h, then xk's, in elements.
+ *   xq_scale, xk_scale
+ *              both NULL, or fp32 [B, N, heads] scales: xq, xk are then int8
+ *              codes (dsa_pack8's rows; strides multiples of 8) and dt is the
+ *              type of q and k.
+ *   wq, wk     fp32 [D] weights; NULL = ones.
+ *   eps        >= 0, finite.  (With eps = 0 a row of zeros comes out NaN.)
+ *   table      device, fp32: the axes' dsa_rope_table tables, 8-byte aligned.
+ *   pos        device, int32 [B or 1, N, 3]: each token's position on each
+ *              axis.  Below 0: that axis' pairs do not turn (text tokens).
+ *   pos_per_batch  1: pos has B entries; 0: one for all of them.
+ *   axes       host, int32 [6]: pairs[3], then the tables' lengths len[3];
+ *              pairs >= 0 with a sum of at most D/2, len >= 1 where pairs > 0.
+ *   halves     0 or 1, see above.
+ *   q, k       out, [B, Hq or Hk, N, D] in dt, contiguous, 16-byte aligned.
+ *   xq8, xk8, xq8_scale, xk8_scale
+ *              all NULL, or (with bf16 or fp32 xq, xk) out: the rows of xq and
+ *              xk as dsa_pack8 would keep them, int8 [B, N, heads, D] (8-byte
+ *              aligned) and fp32 [B, N, heads].
+ * Statistics and rotation are in fp32; each output is rounded once.
+ * Errors: DSA_ERR_INVALID_ARG as listed; a position at or past its axis'
+ * length sets the device error word and does not turn.  Outputs must not
+ * overlap inputs.  Limits: D 64 or 128; B*N < 2^31; Hq, Hk 1..65535.
+ */
+dsa_status dsa_qk_norm_rope(const void* xq, const void* xk, const float* xq_scale,
+                            const float* xk_scale, const int64_t* x_strides, dsa_dtype dt, int B,
+                            int N, int Hq, int Hk, int D, const float* wq, const float* wk,
+                            float eps, const float* table, const int32_t* pos, int pos_per_batch,
+                            const int32_t* axes, int halves, void* q, void* k, int8_t* xq8,
+                            float* xq8_scale, int8_t* xk8, float* xk8_scale, void* stream);
+
+/*
+ * Gradient of dsa_qk_norm_rope.  With g the gradient of y turned back by the
+ * same angles, h = x r and m = mean(g w h) over the row:
+ *   dx = r (g w - h m),   dw = sum over all rows of g h.
+ *
+ *   dq, dk     [B, Hq or Hk, N, D] in dt: gradients of q and k.
+ *   xq .. x_strides, dt, wq .. halves  as in the forward (x as it was given
+ *              there, or the 8-bit rows it left behind, with their scales).
+ *   dxq, dxk   out, [B, N, heads, D] in dt, written through `dx_strides`
+ *              (host, int64 [6], as x_strides; no two rows may overlap).
+ *   dwq, dwk   out, fp32 [D]; each may be NULL.
+ *   workspace  >= dsa_qk_norm_rope_bwd_workspace_size(D) bytes, 16-byte
+ *              aligned.
+ * dw is summed in a fixed order: two calls give the same bits.
+ */
+dsa_status dsa_qk_norm_rope_bwd(const void* dq, const void* dk, const void* xq, const void* xk,
+                                const float* xq_scale, const float* xk_scale,
+                                const int64_t* x_strides, dsa_dtype dt, int B, int N, int Hq,
+                                int Hk, int D, const float* wq, const float* wk, float eps,
+                                const float* table, const int32_t* pos, int pos_per_batch,
+                                const int32_t* axes, int halves, void* dxq, void* dxk,
+                                const int64_t* dx_strides, float* dwq, float* dwk,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* Device workspace bytes for dsa_qk_norm_rope_bwd; 0 for an unsupported D. */
+size_t dsa_qk_norm_rope_bwd_workspace_size(int D);
+
+/*
+ * Activation rows kept in 8 bits between the forward and the backward.  (No
+ * counterpart in the papers; DSV's abstract trains at 520k tokens, where the
+ * activations kept for the backward are what fills the memory.)
+ *
+ *   scale = amax / 127,  code = round-half-even(x * (127 / amax)),
+ * each operation rounded to fp32; the value held is code * scale, off by at
+ * most amax / 254 and fp32 rounding.  A row with a NaN or an infinity gets
+ * scale NaN (it comes back as NaN); one with amax below 2^-119 is held as
+ * zeros.
+ *
+ *   x       [rows, D] in dt, contiguous, 16-byte aligned (unpack: out).
+ *   codes   int8 [rows, D], 8-byte aligned;  scales  fp32 [rows].
+ *   rows    1 .. 2^36.  D 64 or 128.
+ */
+dsa_status dsa_pack8(const void* x, dsa_dtype dt, size_t rows, int D, int8_t* codes,
+                     float* scales, void* stream);
+dsa_status dsa_unpack8(const int8_t* codes, const float* scales, dsa_dtype dt, size_t rows, int D,
+                       void* x, void* stream);
 
 /* Largest `rows` that dsa_select_topp_static accepts. */
 #define DSA_STATIC_MAX_ROWS 32768
