@@ -46,6 +46,13 @@ SIGNATURES = {
                                   _vp, _f, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                   _vp]),
     "dsa_qk_norm_rope_bwd_workspace_size": (_sz, [_i]),
+    "dsa_window_attn_fwd": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i, _i, _i, _vp,
+                                 _vp, _vp]),
+    "dsa_window_attn_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i,
+                                 _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dsa_window_attn_bwd_workspace_size": (_sz, [_i, _i, _i]),
+    "dsa_window_attn_decode": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _i,
+                                    _vp, _vp, _vp]),
     "dsa_pack8": (_i, [_vp, _i, _sz, _i, _vp, _vp, _vp]),
     "dsa_unpack8": (_i, [_vp, _vp, _i, _sz, _i, _vp, _vp]),
     "dsa_select_topp_static": (_i, [_vp, _i, _i, _f, _vp, _vp, _vp, _vp, _vp]),

@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libdsa.so")
 SOURCES = ["dsa_api.cu", "pool_score.cu", "select_topp.cu", "attn_sm100.cu",
            "attn_simt.cu", "block_mass.cu", "select_static.cu", "reorder.cu",
            "attn_bwd.cu", "attn_bwd_sm100.cu", "selftest.cu", "layer_api.cu",
-           "qk_norm_rope.cu", "act8.cu"]
+           "qk_norm_rope.cu", "act8.cu", "window_fwd_sm100.cu", "window_bwd_sm100.cu",
+           "window_simt.cu", "window_decode.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -338,6 +338,27 @@ cudaError_t launch_grads_t(int D, int block, const void* q, const void* k, const
 
 }  // namespace
 
+cudaError_t launch_row_delta(const void* out, const void* dout, bool bf16, long long rows, int D,
+                             float* delta, cudaStream_t s) {
+  const int dgrid = (int)((rows + 7) / 8);
+  if (bf16) {
+    if (D == 64)
+      delta_kernel<__nv_bfloat16, 64><<<dgrid, 256, 0, s>>>(
+          static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), rows, delta);
+    else
+      delta_kernel<__nv_bfloat16, 128><<<dgrid, 256, 0, s>>>(
+          static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), rows, delta);
+  } else {
+    if (D == 64)
+      delta_kernel<float, 64><<<dgrid, 256, 0, s>>>(static_cast<const float*>(out),
+                                                     static_cast<const float*>(dout), rows, delta);
+    else
+      delta_kernel<float, 128><<<dgrid, 256, 0, s>>>(static_cast<const float*>(out),
+                                                      static_cast<const float*>(dout), rows, delta);
+  }
+  return cudaGetLastError();
+}
+
 cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                             const void* dout, const float* lse, bool bf16, int BH, int N, int D,
                             int block, float scale, const int32_t* row_ptr,
@@ -354,24 +375,7 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const v
   if ((e = launch_csr_scan(counts, rows, t_row_ptr, s)) != cudaSuccess) return e;
   mask_transpose_kernel<<<ceil_div(rows, 8), 256, 0, s>>>(bitmap, BH, nB, t_row_ptr, counts,
                                                           t_col);
-  const long long tok = (long long)BH * N;
-  const int dgrid = (int)((tok + 7) / 8);
-  if (bf16) {
-    if (D == 64)
-      delta_kernel<__nv_bfloat16, 64><<<dgrid, 256, 0, s>>>(
-          static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), tok, delta);
-    else
-      delta_kernel<__nv_bfloat16, 128><<<dgrid, 256, 0, s>>>(
-          static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), tok, delta);
-  } else {
-    if (D == 64)
-      delta_kernel<float, 64><<<dgrid, 256, 0, s>>>(static_cast<const float*>(out),
-                                                     static_cast<const float*>(dout), tok, delta);
-    else
-      delta_kernel<float, 128><<<dgrid, 256, 0, s>>>(static_cast<const float*>(out),
-                                                      static_cast<const float*>(dout), tok, delta);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_row_delta(out, dout, bf16, (long long)BH * N, D, delta, s)) != cudaSuccess) return e;
   // bf16 with blocks of 128: the tensor-core kernels; otherwise exact fp32 on CUDA cores
   if (bf16 && block == 128)
     return launch_attn_bwd_sm100(q, k, v, dout, lse, delta, BH, N, D, scale, row_ptr, col_idx,

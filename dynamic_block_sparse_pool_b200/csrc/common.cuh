@@ -85,6 +85,9 @@ cudaError_t launch_attn_bwd(const void* q, const void* k, const void* v, const v
                             const int32_t* col_idx, void* dq, void* dk, void* dv,
                             uint32_t* bitmap, int32_t* counts, int32_t* t_row_ptr,
                             int32_t* t_col, float* delta, unsigned* err, cudaStream_t s);
+// rowsum(dO * O) of `rows` rows of D values.
+cudaError_t launch_row_delta(const void* out, const void* dout, bool bf16, long long rows, int D,
+                             float* delta, cudaStream_t s);
 // dQ, dK, dV on tcgen05 (bf16, blocks of 128): after the mask transpose and
 // the row term delta of launch_attn_bwd.
 cudaError_t launch_attn_bwd_sm100(const void* q, const void* k, const void* v, const void* dout,

@@ -2,6 +2,7 @@
 // per-head norm with rotation, the window attention and the 8-bit activation
 // rows.  Argument checks and dispatch; no call allocates device memory or
 // synchronises the host.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -9,6 +10,7 @@
 
 #include "dsa.h"
 #include "norm_rope.cuh"
+#include "window_attn.cuh"
 
 namespace dsa {
 dsa_status api_checked_device(unsigned** err_word);
@@ -30,6 +32,13 @@ dsa_status fail(dsa_status st, const char* fmt, ...) {
 
 dsa_status launched(cudaError_t e, const char* where) {
   return e == cudaSuccess ? DSA_OK : fail(DSA_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
+
+dsa_status sm_count(int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  return launched(e, "cudaDeviceGetAttribute");
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -92,9 +101,132 @@ dsa::RopeArgs rope_args(const float* table, const int32_t* pos, int pos_per_batc
   return r;
 }
 
+dsa_status check_heads(int B, int H, int Hk, int D, float scale, int sink, dsa_dtype dt) {
+  if (!known(dt)) return fail(DSA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+  if (B < 1 || H < 1 || Hk < 1) return fail(DSA_ERR_INVALID_ARG, "B, H, Hk must be >= 1 (got %d, %d, %d)", B, H, Hk);
+  if ((long long)B * H > 65535) return fail(DSA_ERR_INVALID_ARG, "B*H = %lld exceeds 65535", (long long)B * H);
+  if (H % Hk) return fail(DSA_ERR_INVALID_ARG, "H = %d must be a multiple of Hk = %d", H, Hk);
+  if (D != 64 && D != 128) return fail(DSA_ERR_INVALID_ARG, "head_dim D must be 64 or 128 (got %d)", D);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(DSA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (sink < 0) return fail(DSA_ERR_INVALID_ARG, "sink must be >= 0 (got %d)", sink);
+  return DSA_OK;
+}
+
+int bound(int v) { return v < 0 || v > dsa::Window::kNoBound ? dsa::Window::kNoBound : v; }
+
+// Checks and arguments that the window attention's passes share.
+dsa_status window_args(dsa::WindowAttn& a, const void* q, const void* k, const void* v, dsa_dtype dt, int B, int H,
+                       int Hk, int Nq, int Nk, int D, float scale, int q_offset, int left, int right, int sink) {
+  dsa_status st = check_heads(B, H, Hk, D, scale, sink, dt);
+  if (st != DSA_OK) return st;
+  if (Nq < 1 || Nk < 1 || Nq > (1 << 27) || Nk > (1 << 27))
+    return fail(DSA_ERR_INVALID_ARG, "Nq and Nk must be 1..2^27 (got %d, %d)", Nq, Nk);
+  if (q_offset > (1 << 28) || q_offset < -(1 << 28))
+    return fail(DSA_ERR_INVALID_ARG, "q_offset must be within 2^28 of 0 (got %d)", q_offset);
+  const long long tiles = (std::max(Nq, Nk) + 63ll) / 64;
+  if ((long long)B * H * tiles > INT_MAX) return fail(DSA_ERR_INVALID_ARG, "too many query or key tiles");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+  a = {};
+  a.B = B; a.H = H; a.Hk = Hk; a.D = D;
+  a.w = {Nq, Nk, q_offset, bound(left), bound(right), std::min(sink, Nk)};
+  a.scale = scale;
+  a.q = q; a.k = k; a.v = v;
+  if ((st = dsa::api_checked_device(&a.err)) != DSA_OK) return st;
+  return sm_count(&a.num_sms);
+}
+
 }  // namespace
 
 extern "C" {
+
+dsa_status dsa_window_attn_fwd(const void* q, const void* k, const void* v, dsa_dtype dt, int B,
+                               int H, int Hk, int Nq, int Nk, int D, float scale, int q_offset,
+                               int left, int right, int sink, void* out, float* lse,
+                               void* stream) {
+  dsa::api_set_last_error("");
+  if (!q || !k || !v || !out) return fail(DSA_ERR_INVALID_ARG, "null q, k, v or out");
+  if (!aligned(out, 16) || !aligned(lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "out must be 16-byte aligned, lse 4-byte aligned");
+  dsa::WindowAttn a;
+  dsa_status st = window_args(a, q, k, v, dt, B, H, Hk, Nq, Nk, D, scale, q_offset, left, right, sink);
+  if (st != DSA_OK) return st;
+  a.out = out;
+  a.lse = lse;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const char* why = nullptr;
+  const cudaError_t e = dt == DSA_BF16 ? dsa::launch_window_fwd_sm100(a, s, &why) : dsa::launch_window_fwd_simt(a, s);
+  if (e != cudaSuccess && why) return fail(DSA_ERR_CUDA, "window_attn_fwd: %s", why);
+  return launched(e, "window_attn_fwd launch");
+}
+
+size_t dsa_window_attn_bwd_workspace_size(int B, int H, int Nq) {
+  if (B < 1 || H < 1 || Nq < 1) return 0;
+  return ((size_t)B * H * Nq * sizeof(float) + 15) / 16 * 16;
+}
+
+dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                               const void* dout, const float* lse, dsa_dtype dt, int B, int H,
+                               int Hk, int Nq, int Nk, int D, float scale, int q_offset, int left,
+                               int right, int sink, void* dq, void* dk, void* dv, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  dsa::api_set_last_error("");
+  if (!q || !k || !v || !out || !dout || !lse || !dq || !dk || !dv || !workspace)
+    return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(out, 16) || !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
+      !aligned(workspace, 16) || !aligned(lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "tensors and workspace must be 16-byte aligned, lse 4-byte aligned");
+  dsa::WindowAttn a;
+  dsa_status st = window_args(a, q, k, v, dt, B, H, Hk, Nq, Nk, D, scale, q_offset, left, right, sink);
+  if (st != DSA_OK) return st;
+  if (ws_bytes < dsa_window_attn_bwd_workspace_size(B, H, Nq))
+    return fail(DSA_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu needed", ws_bytes,
+                dsa_window_attn_bwd_workspace_size(B, H, Nq));
+  a.o = out; a.dout = dout;
+  a.lse = const_cast<float*>(lse);
+  a.dq = dq; a.dk = dk; a.dv = dv;
+  a.delta = static_cast<float*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const char* why = nullptr;
+  cudaError_t e = dsa::launch_row_delta(out, dout, dt == DSA_BF16, (long long)B * H * Nq, D, a.delta, s);
+  if (e == cudaSuccess)
+    e = dt == DSA_BF16 ? dsa::launch_window_bwd_sm100(a, s, &why) : dsa::launch_window_bwd_simt(a, s);
+  if (e != cudaSuccess && why) return fail(DSA_ERR_CUDA, "window_attn_bwd: %s", why);
+  return launched(e, "window_attn_bwd launch");
+}
+
+dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
+                                  const int64_t* kv_strides, dsa_dtype dt, int B, int H, int Hk,
+                                  int Nq, int cap, int D, float scale, const int32_t* lens,
+                                  int left, int sink, void* out, float* lse, void* stream) {
+  dsa::api_set_last_error("");
+  if (!q || !k || !v || !kv_strides || !lens || !out)
+    return fail(DSA_ERR_INVALID_ARG, "null q, k, v, kv_strides, lens or out");
+  dsa_status st = check_heads(B, H, Hk, D, scale, sink, dt);
+  if (st != DSA_OK) return st;
+  if (Nq < 1 || Nq > 128) return fail(DSA_ERR_INVALID_ARG, "Nq must be 1..128 (got %d)", Nq);
+  if (cap < 1 || cap > (1 << 27)) return fail(DSA_ERR_INVALID_ARG, "cap must be 1..2^27 (got %d)", cap);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lens, 4) ||
+      !aligned(lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned, lens and lse 4-byte aligned");
+  if ((st = check_strides(kv_strides, dt == DSA_BF16 ? 8 : 4, "kv_strides")) != DSA_OK) return st;
+  dsa::DecodeAttn a = {};
+  a.B = B; a.H = H; a.Hk = Hk; a.group = H / Hk; a.Nq = Nq; a.cap = cap;
+  a.scale = scale;
+  a.left = bound(left);
+  a.sink = std::min(sink, cap);
+  a.q = q; a.k = k; a.v = v;
+  for (int i = 0; i < 3; ++i) {
+    a.ks[i] = kv_strides[i];
+    a.vs[i] = kv_strides[3 + i];
+  }
+  a.lens = lens;
+  a.out = out;
+  a.lse = lse;
+  if ((st = dsa::api_checked_device(&a.err)) != DSA_OK || (st = sm_count(&a.num_sms)) != DSA_OK) return st;
+  return launched(dsa::launch_window_decode(a, dt == DSA_BF16, D, static_cast<cudaStream_t>(stream)),
+                  "window_attn_decode launch");
+}
 
 dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table) {
   dsa::api_set_last_error("");

@@ -1,0 +1,490 @@
+// Window attention forward on Blackwell tensor cores (sm_100a), bf16,
+// D = 64 or 128: TMA loads, tcgen05 MMAs with fp32 accumulators in tensor
+// memory, online softmax on CUDA cores, warp-specialised and persistent.
+//
+// For every query: softmax over its visible keys (window.cuh), in one pass
+// over key tiles of 128 with a running reference m and sum l:
+//   P = 2^(S scale log2e - m),  l += rowsum(P),  O += P V;  O / l at the end.
+// m only moves when a tile's maximum exceeds it by more than 8 (base 2), and
+// then l and O are rescaled: P stays below 2^8, where bf16 and fp32 are as
+// precise as below 1, and O and l share the reference, so the result is the
+// softmax all the same.  P is rounded to bf16 for the second product (at most
+// half a step, 2^-9 of each weight; l sums the unrounded values).
+//
+// An item is two neighbouring tiles of 128 queries of one head (one, where
+// items would not fill the SMs), so a key tile in shared memory serves both
+// and shared-memory traffic per MMA stays below what the tensor cores need.
+// One CTA per SM takes items blockIdx.x, blockIdx.x + gridDim.x, ... (items of
+// one head follow one another: CTAs that run at the same time read
+// overlapping windows, which L2 holds).  384 threads:
+//   warps 0-3  softmax and output of query tile A, one row per thread
+//   warps 4-7  the same for tile B
+//   warp  8    MMA issuer (and tensor-memory allocation)
+//   warp  9    TMA loader: the two Q tiles, then K and V tiles through a ring
+//   (warps 10 and 11 only complete the warpgroup that gives registers up)
+// Tensor memory: S_A, S_B (128 columns each; P overwrites S in place as
+// packed bf16), O_A, O_B.  While tile A is in its softmax the tensor cores
+// run tile B's PV and next S, and the other way round.  The MMAs of one
+// thread run in order, so S(i+1) overwrites the buffer of P(i) after PV(i)
+// has read it, and a finished S(i+1) also means that PV(i) is done: the
+// softmax warps may rescale O, and after the last PV read it out, without
+// another barrier; the next item's first PV waits for their P, which they
+// write after they have read O.
+//
+// Masks: a key tile that every row of the query tile sees in full needs
+// none; in the others hidden scores become -inf before the maximum, so what
+// a hidden key holds (NaN included) does not matter for S.  A row whose keys
+// are all hidden so far keeps m = -inf and uses 0 in its place, so its P is 0.
+// Every mbarrier wait is bounded; a timeout sets the device error word and
+// the CTA winds down.
+#include "sm100.cuh"
+#include "tile_map.cuh"
+#include "window.cuh"
+#include "window_attn.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128, BN = 128;
+constexpr int kThreads = 384;
+// Registers: 12 warps get 168 each at launch (64,512 in all); the softmax
+// warps, which hold a row of S, take 208, the others keep 88 (256 * 208 +
+// 128 * 88 = 64,512).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kStep = 8.f;  // the reference moves when a maximum exceeds it by more
+
+// Pairs of the 16 in each chunk of 32 keys whose exponentials run on the FMA
+// pipe instead of the MUFU.
+template <int D>
+constexpr int poly_pairs() { return 0; }
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = BM * D * 2;        // one [128 x D] bf16 tile
+  static constexpr int kSub = BM * 64 * 2;        // one 128B-swizzled [128 x 64] part
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kQ = 0;                    // two tiles
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kBar = kRing + kStages * kTile;
+  // barriers: Q landed, Q free, ring landed / free, S (or the last PV) done
+  // per query tile, P written per query tile and half
+  static constexpr int kQFull = 0, kQFree = 1, kFull = 2, kFree = kFull + kStages,
+                       kS = kFree + kStages, kP = kS + 2, kDrain = kP + 4, kNumBars = kDrain + 1;
+  static constexpr int kSlot = kBar + 8 * kNumBars;
+  static constexpr int kBytes = kSlot + 16;
+};
+
+__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ float exp2_mufu(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct FwdParams {
+  Window w;
+  int H, group;       // query heads, query heads per key head
+  int pairs;          // query tiles per item (1 or 2)
+  int items_per_head;
+  int items;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+};
+
+// An item: head, first query, the key tiles of each query tile and of both.
+struct Item {
+  int bh, kv, q0;
+  KeyTiles<BN> a, b, all;
+  __device__ __forceinline__ Item(const FwdParams& p, int i) {
+    bh = i / p.items_per_head;
+    q0 = (i - bh * p.items_per_head) * (BM * p.pairs);
+    kv = bh / p.group;  // (b H + h) / group = b Hk + h / group
+    a = KeyTiles<BN>::of(p.w, q0, min(q0 + BM, p.w.Nq));
+    b = p.pairs == 2 ? KeyTiles<BN>::of(p.w, q0 + BM, min(q0 + 2 * BM, p.w.Nq)) : KeyTiles<BN>::none();
+    all = KeyTiles<BN>::join(a, b);
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int row, int head,
+                                          uint32_t bar) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * Smem<D>::kSub, map, c * 64, row, head, bar);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const FwdParams p, unsigned* err) {
+  using L = Smem<D>;
+  constexpr int ST = L::kStages;
+  constexpr uint32_t kTileBytes = L::kTile;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  if (base & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) flag_error(err, kErrAlign);
+    return;
+  }
+  const uint32_t bars = base + L::kBar;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i >= L::kP && i < L::kP + 4 ? 4u : 1u);
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint32_t issued = 0, q_issued = 0;  // loader: ring tiles and Q loads issued
+  bool had_mma = false;
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ loader
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        const Item it(p, i);
+        const int n = it.all.count();
+        if (n == 0) continue;
+        // Q's buffer is free once every S of the previous item is done
+        if (q_issued > 0 && !(ok = mbar_wait(bar(L::kQFree), (q_issued - 1) & 1u) && !*abort_flag)) break;
+        const bool two = it.b.count() > 0;
+        mbar_expect_tx(bar(L::kQFull), two ? 2 * kTileBytes : kTileBytes);
+        load_tile<D>(base + L::kQ, &tmQ, it.q0, it.bh, bar(L::kQFull));
+        if (two) load_tile<D>(base + L::kQ + kTileBytes, &tmQ, it.q0 + BM, it.bh, bar(L::kQFull));
+        ++q_issued;
+        // K(0), then K(e), V(e - 1) in the order the MMA issuer takes them
+        for (int e = 0; e <= 2 * n - 1 && ok; ++e) {
+          const bool is_k = e == 0 || ((e & 1) && e < 2 * n - 1);
+          const int blk = is_k ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1;
+          const uint32_t s = issued % ST;
+          if (!(ok = mbar_wait(bar(L::kFree + s), ((issued / ST) & 1u) ^ 1u) && !*abort_flag)) break;
+          mbar_expect_tx(bar(L::kFull + s), kTileBytes);
+          load_tile<D>(base + L::kRing + s * kTileBytes, is_k ? &tmK : &tmV, it.all.tile(blk) * BN, it.kv,
+                       bar(L::kFull + s));
+          ++issued;
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(err, kErrTimeout);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------- MMA issuer
+    const bool leader = lane == 0;
+    constexpr uint32_t kIdescS = idesc_bf16_f32(BM, BN, false);
+    constexpr uint32_t kIdescO = idesc_bf16_f32(BM, D, true);
+    const uint64_t dq = smem_desc_sw128(base + L::kQ, 16, 1024);
+    const uint64_t dk = smem_desc_sw128(base + L::kRing, 16, 1024);
+    const uint64_t dv = smem_desc_sw128(base + L::kRing, L::kSub, 1024);
+    auto kstep = [](int kk) -> uint64_t {  // 16 columns of D in a K-major tile
+      return (uint64_t)(((kk >> 2) * L::kSub + (kk & 3) * 32) >> 4);
+    };
+    uint32_t pos = 0;                   // ring tiles taken so far
+    uint32_t p_seen[2] = {0u, 0u};      // P tiles taken of each query tile
+    uint32_t q_seen = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      const Item it(p, i);
+      const int n = it.all.count();
+      if (n == 0) continue;
+      if (!(ok = warp_all(mbar_wait(bar(L::kQFull), q_seen & 1u)))) break;
+      ++q_seen;
+      had_mma = true;
+      // the last key tile of each query tile (-1: none)
+      int last_a = n - 1, last_b = n - 1;
+      while (last_a >= 0 && !it.a.has(it.all.tile(last_a))) --last_a;
+      while (last_b >= 0 && !it.b.has(it.all.tile(last_b))) --last_b;
+      bool pend[2] = {false, false}, started[2] = {false, false};
+      for (int e = 0; e <= n && ok; ++e) {
+        const int j = e < n ? it.all.tile(e) : -1;
+        // ring order: K(0), K(1), V(0), K(2), V(1), ..., V(n - 1)
+        const uint32_t k_at = e == 0 ? pos : pos + 2 * e - 1;
+        const uint32_t v_at = e == n ? pos + 2 * n - 1 : pos + 2 * e;  // V(e - 1), e >= 1
+        const uint32_t ks = k_at % ST, vs = v_at % ST;
+        if (e < n && !(ok = warp_all(mbar_wait(bar(L::kFull + ks), (k_at / ST) & 1u)))) break;
+        bool v_here = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t tS = tmem + 128u * x, tO = tmem + kColO + (uint32_t)D * x;
+          const bool act = e < n && (x ? it.b : it.a).has(j);
+          if (!act && !pend[x]) continue;
+          if (pend[x]) {
+            // O (+)= P(e - 1) V(e - 1), a half of the keys at a time
+            if (!v_here && !(ok = warp_all(mbar_wait(bar(L::kFull + vs), (v_at / ST) & 1u)))) break;
+            v_here = true;
+            const uint64_t v0 = dv + (uint64_t)((vs * kTileBytes) >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!(ok = ok && warp_all(mbar_wait(bar(L::kP + 2 * x + h), p_seen[x] & 1u)))) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                  mma_ts(tO, tS + 8u * kk, v0 + (uint64_t)((kk * 2048) >> 4), kIdescO,
+                         started[x] || kk > 0 ? 1u : 0u);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            ++p_seen[x];
+            started[x] = true;
+            pend[x] = false;
+          }
+          if (act) {
+            if (leader) {
+              const uint64_t k0 = dk + (uint64_t)((ks * kTileBytes) >> 4);
+              const uint64_t q0 = dq + (uint64_t)((x * kTileBytes) >> 4);
+              mma_ss(tS, q0, k0, kIdescS, 0u);
+#pragma unroll
+              for (int kk = 1; kk < D / 16; ++kk) mma_ss_acc(tS, q0 + kstep(kk), k0 + kstep(kk), kIdescS);
+            }
+            pend[x] = true;
+          }
+          // S(e) is done, or the tile's last PV
+          if (leader && (act || e > (x ? last_b : last_a))) mma_commit(bar(L::kS + x));
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) {
+          if (e < n) mma_commit(bar(L::kFree + ks));
+          if (e > 0) mma_commit(bar(L::kFree + vs));
+          if (e == n - 1) mma_commit(bar(L::kQFree));
+        }
+        __syncwarp();
+      }
+      pos += 2 * n;
+    }
+    if (!ok && leader) {
+      *abort_flag = 1;
+      flag_error(err, kErrTimeout);
+    }
+  }
+  } else {
+    // ----------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int x = warp >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lane_off + 128u * x, tO = tmem + lane_off + kColO + (uint32_t)D * x;
+    const float scale = p.scale_log2;
+    uint32_t seen = 0;  // phases of S done taken so far
+    bool ok = true;
+    for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      const Item it(p, i);
+      const KeyTiles<BN> mine = x ? it.b : it.a;
+      const int q0 = it.q0 + BM * x, q1 = min(q0 + BM, p.w.Nq);
+      if (q0 >= q1 || x >= p.pairs) continue;
+      const int t = p.w.off + q0 + row;
+      const int lo = p.w.lo(t), hi = p.w.hi(t);
+      const int n = mine.count();
+      float mref = -INFINITY, l = 0.f;
+      for (int e = 0; e < n; ++e) {
+        const int k0 = mine.tile(e) * BN;
+        if (!(ok = warp_all(mbar_wait(bar(L::kS + x), seen & 1u)))) break;
+        ++seen;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
+        if (!all_visible(p.w, q0, q1, k0, k0 + BN)) {
+          const int chi = hi - k0, clo = lo - k0, csk = p.w.sink - k0;
+          auto below = [](int v) { return v <= 0 ? 0u : v >= 32 ? 0xffffffffu : (1u << v) - 1u; };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t m = below(chi - 32 * c) & (~below(clo - 32 * c) | below(csk - 32 * c));
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              if (!((m >> u) & 1u)) s[c][u] = 0xff800000u;  // -inf
+          }
+        }
+        float m4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          m4[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int u = 1; u + 1 < 32; u += 2)
+            m4[c] = max3f(m4[c], __uint_as_float(s[c][u]), __uint_as_float(s[c][u + 1]));
+          m4[c] = fmaxf(m4[c], __uint_as_float(s[c][31]));
+        }
+        const float m = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
+        const bool move = m > mref + kStep || (mref == -INFINITY && m > mref);
+        if (__any_sync(0xffffffffu, move)) {
+          const float alpha = move ? exp2f(mref - m) : 1.f;  // 0 where the row had no keys yet
+          if (move) mref = m;
+          l *= alpha;
+          if (e > 0) {
+            // O holds the sum through the previous key tile
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * c, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+              tmem_st32(tO + 32 * c, o);
+            }
+          }
+        }
+        const float nm = mref == -INFINITY ? 0.f : -mref;
+        const uint64_t sc2 = pack_f32x2(scale, scale), nm2 = pack_f32x2(nm, nm);
+        uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(s[c][2 * u]), __uint_as_float(s[c][2 * u + 1])),
+                                   sc2, nm2);
+            if ((u + 1) * poly_pairs<D>() / 16 != u * poly_pairs<D>() / 16) {
+              y = exp2_poly_x2(y);
+            } else {
+              float a, b;
+              unpack_f32x2(y, a, b);
+              y = pack_f32x2(exp2_mufu(a), exp2_mufu(b));
+            }
+            sum2[u & 1] = add_f32x2(sum2[u & 1], y);
+            float a, b;
+            unpack_f32x2(y, a, b);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+            pk[u] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          tmem_st16(tS + 16 * c, pk);
+          if (c & 1) {  // half of the keys: the MMA issuer may start on them
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kP + 2 * x + (c >> 1)));
+          }
+        }
+        float a, b;
+        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), a, b);
+        l += a + b;
+      }
+      if (!ok) break;
+      // O is complete with the next phase of S done
+      if (n > 0) {
+        if (!(ok = warp_all(mbar_wait(bar(L::kS + x), seen & 1u)))) break;
+        ++seen;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
+      const bool valid = q0 + row < q1;
+      const size_t tok = (size_t)it.bh * p.w.Nq + q0 + row;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld_regs(o);
+        }
+#pragma unroll
+        for (int w8 = 0; w8 < 4; ++w8) {
+          uint32_t h[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float a = __uint_as_float(o[8 * w8 + 2 * u]) * inv, b = __uint_as_float(o[8 * w8 + 2 * u + 1]) * inv;
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+            h[u] = l == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          if (valid)
+            *reinterpret_cast<uint4*>(p.out + tok * D + 32 * c + 8 * w8) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      if (valid && p.lse) p.lse[tok] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
+      tc_fence_before();
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) flag_error(err, kErrTimeout);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // A role gave up: let every copy and MMA in flight finish (bounded)
+    // before shared and tensor memory are released.
+    if (warp == kMmaWarp && had_mma) {
+      if (lane == 0) {
+        mma_commit(bar(L::kDrain));
+        mbar_wait(bar(L::kDrain), 0u);
+      }
+      __syncwarp();
+    } else if (warp == kLoadWarp && lane == 0) {
+      for (uint32_t b = issued > ST ? issued - ST : 0; b < issued; ++b)
+        mbar_wait(bar(L::kFull + b % ST), (b / ST) & 1u);
+      if (q_issued > 0) mbar_wait(bar(L::kQFull), (q_issued - 1) & 1u);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                     const FwdParams& p, int num_sms, unsigned* err, cudaStream_t s) {
+  const int smem = Smem<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  window_fwd_kernel<D><<<min(p.items, num_sms), kThreads, smem, s>>>(mq, mk, mv, p, err);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why) {
+  const int BH = a.B * a.H;
+  CUtensorMap mq, mk, mv;
+  if (!make_bf16_tile_map(&mq, a.q, BH, a.w.Nq, a.D) || !make_bf16_tile_map(&mk, a.k, a.B * a.Hk, a.w.Nk, a.D) ||
+      !make_bf16_tile_map(&mv, a.v, a.B * a.Hk, a.w.Nk, a.D)) {
+    if (why) *why = "cuTensorMapEncodeTiled failed or is unavailable";
+    return cudaErrorInvalidValue;
+  }
+  FwdParams p;
+  p.w = a.w;
+  p.H = a.H;
+  p.group = a.H / a.Hk;
+  // two query tiles per item, unless single ones are needed to fill the SMs
+  const int tiles = ceil_div(a.w.Nq, BM);
+  p.pairs = (long long)BH * ceil_div(tiles, 2) >= a.num_sms ? 2 : 1;
+  p.items_per_head = ceil_div(tiles, p.pairs);
+  p.items = BH * p.items_per_head;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  return a.D == 64 ? launch_d<64>(mq, mk, mv, p, a.num_sms, a.err, s)
+                   : launch_d<128>(mq, mk, mv, p, a.num_sms, a.err, s);
+}
+
+}  // namespace dsa

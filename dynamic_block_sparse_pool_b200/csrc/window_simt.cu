@@ -1,0 +1,350 @@
+// Window attention in exact fp32 on CUDA cores: forward and backward.
+//
+// Serves fp32 inputs, where a tf32 or bf16 product would miss fp32 results.
+// One CTA (256 threads) per tile of 64 queries (forward, dQ) or 64 keys (dK,
+// dV); the tiles of the other side stream through shared memory.  Bound by
+// the FMA pipe: thread (ty, tx) of 16 x 16 owns rows ty + 16 a and columns tx
+// + 16 b (a, b < 4) of every 64 x 64 product, read from shared memory as
+// float4 along the summed dimension, 8 loads for 64 FMAs.  Rows are padded to
+// D + 4 (64 + 4) floats, so the 16 columns of a load fall in different banks.
+//
+// Formulas as in window_fwd_sm100.cu and window_bwd_sm100.cu.  dK and dV of a
+// key head are summed over its query heads and queries in a fixed order by
+// one CTA: no atomics, equal bits from run to run.
+#include <algorithm>
+
+#include "window_attn.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int T = 64;        // queries and keys of a tile
+constexpr int SP = T + 4;    // padded row of a 64 x 64 tile
+constexpr int kThreads = 256;
+
+template <int D>
+constexpr int padded() { return D + 4; }
+
+// Rows r0 .. r0 + 63 of a [rows, D] head into shared memory; rows past `end`
+// read as zeros.
+template <int D>
+__device__ __forceinline__ void stage(float* dst, const float* __restrict__ src, int r0, int end) {
+  constexpr int V = D / 4;
+  for (int i = threadIdx.x; i < T * V; i += kThreads) {
+    const int r = i / V, c = 4 * (i - r * V);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < end) v = *reinterpret_cast<const float4*>(src + (size_t)(r0 + r) * D + c);
+    *reinterpret_cast<float4*>(dst + r * padded<D>() + c) = v;
+  }
+}
+
+// acc[a][b] += A[ty + 16 a] . B[tx + 16 b] over D columns
+template <int D>
+__device__ __forceinline__ void product_nt(float (&acc)[4][4], const float* A, const float* B, int ty, int tx) {
+  constexpr int P = padded<D>();
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4*>(A + (ty + 16 * a) * P + d);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) y[b] = *reinterpret_cast<const float4*>(B + (tx + 16 * b) * P + d);
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        acc[a][b] = fmaf(x[a].x, y[b].x, acc[a][b]);
+        acc[a][b] = fmaf(x[a].y, y[b].y, acc[a][b]);
+        acc[a][b] = fmaf(x[a].z, y[b].z, acc[a][b]);
+        acc[a][b] = fmaf(x[a].w, y[b].w, acc[a][b]);
+      }
+  }
+}
+
+// acc[a][4 g + u] += sum over k of W[ty + 16 a][k] B[k][64 g + 4 tx + u]
+template <int D>
+__device__ __forceinline__ void product_nn(float (&acc)[4][D / 16], const float* W, const float* B, int ty, int tx) {
+  constexpr int P = padded<D>();
+#pragma unroll 2
+  for (int k = 0; k < T; k += 4) {
+    float w[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const float4 v = *reinterpret_cast<const float4*>(W + (ty + 16 * a) * SP + k);
+      w[a][0] = v.x; w[a][1] = v.y; w[a][2] = v.z; w[a][3] = v.w;
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) {
+        const float4 y = *reinterpret_cast<const float4*>(B + (k + kk) * P + 64 * g + 4 * tx);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          acc[a][4 * g] = fmaf(w[a][kk], y.x, acc[a][4 * g]);
+          acc[a][4 * g + 1] = fmaf(w[a][kk], y.y, acc[a][4 * g + 1]);
+          acc[a][4 * g + 2] = fmaf(w[a][kk], y.z, acc[a][4 * g + 2]);
+          acc[a][4 * g + 3] = fmaf(w[a][kk], y.w, acc[a][4 * g + 3]);
+        }
+      }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_rows(float* dst, const float (&acc)[4][D / 16], int r0, int end, float (&mul)[4],
+                                           int ty, int tx) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int r = r0 + ty + 16 * a;
+    if (r < end)
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g)
+        *reinterpret_cast<float4*>(dst + (size_t)r * D + 64 * g + 4 * tx) =
+            make_float4(acc[a][4 * g] * mul[a], acc[a][4 * g + 1] * mul[a], acc[a][4 * g + 2] * mul[a],
+                        acc[a][4 * g + 3] * mul[a]);
+  }
+}
+
+// Is key u visible to the query at position t?
+__device__ __forceinline__ bool sees(const Window& w, int t, int u) {
+  return u < w.Nk && u <= t + w.right && (u < w.sink || u >= t - w.left);
+}
+
+// sum / max over the 16 threads (tx) of a row
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+window_fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                       const Window w, int group, float scale, float* __restrict__ out, float* __restrict__ lse) {
+  constexpr int P = padded<D>();
+  extern __shared__ __align__(16) float sm[];
+  float* Q = sm;
+  float* KV = Q + T * P;   // K, then V of the same tile
+  float* W = KV + T * P;   // weights
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tiles = ceil_div(w.Nq, T), bh = blockIdx.x / tiles, q0 = (blockIdx.x - bh * tiles) * T;
+  const int q1 = min(q0 + T, w.Nq);
+  const size_t qh = (size_t)bh * w.Nq * D, kh = (size_t)(bh / group) * w.Nk * D;
+  stage<D>(Q, q + qh, q0, w.Nq);
+  float o[4][D / 16], m[4], l[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    m[a] = -INFINITY;
+    l[a] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[a][c] = 0.f;
+  }
+  const KeyTiles<T> kt = KeyTiles<T>::of(w, q0, q1);
+  for (int e = 0; e < kt.count(); ++e) {
+    const int k0 = kt.tile(e) * T;
+    __syncthreads();  // the previous tile's V and weights are consumed
+    stage<D>(KV, k + kh, k0, w.Nk);
+    __syncthreads();
+    float s[4][4] = {};
+    product_nt<D>(s, Q, KV, ty, tx);
+    const bool whole = all_visible(w, q0, q1, k0, k0 + T);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int t = w.off + q0 + ty + 16 * a;
+      float top = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        s[a][b] = whole || sees(w, t, k0 + tx + 16 * b) ? s[a][b] * scale : -INFINITY;
+        top = fmaxf(top, s[a][b]);
+      }
+      const float mn = fmaxf(m[a], max16(top));
+      // a row with no visible key so far keeps m = -inf; 0 in its place makes its weights 0
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      const float alpha = expf(m[a] - mu);
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float x = expf(s[a][b] - mu);
+        W[(ty + 16 * a) * SP + tx + 16 * b] = x;
+        sum += x;
+      }
+      l[a] = l[a] * alpha + sum16(sum);
+      m[a] = mn;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[a][c] *= alpha;
+    }
+    __syncthreads();  // K is consumed, the weights are written
+    stage<D>(KV, v + kh, k0, w.Nk);
+    __syncthreads();
+    product_nn<D>(o, W, KV, ty, tx);
+  }
+  float inv[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) inv[a] = l[a] == 0.f ? 0.f : 1.f / l[a];
+  store_rows<D>(out + qh, o, q0, q1, inv, ty, tx);
+  if (lse && tx == 0)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = q0 + ty + 16 * a;
+      if (r < q1) lse[(size_t)bh * w.Nq + r] = l[a] == 0.f ? -INFINITY : m[a] + logf(l[a]);
+    }
+}
+
+// P and dS of a 64 x 64 tile; hidden pairs, and rows without keys (lse =
+// -inf), have both 0.
+__device__ __forceinline__ void weights(const float (&s)[4][4], const float (&dp)[4][4], float (&p)[4][4],
+                                        float (&ds)[4][4], const Window& w, int q0, int k0, bool whole, float scale,
+                                        const float* lse, const float* delta, int ty, int tx) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int r = ty + 16 * a;
+    const float ls = lse[r], de = delta[r];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const bool in = whole || sees(w, w.off + q0 + r, k0 + tx + 16 * b);
+      p[a][b] = in && ls > -INFINITY ? expf(fmaf(scale, s[a][b], -ls)) : 0.f;
+      ds[a][b] = in && ls > -INFINITY ? p[a][b] * (dp[a][b] - de) : 0.f;
+    }
+  }
+}
+
+__device__ __forceinline__ void stage_vec(float* dst, const float* src, int r0, int end, float pad) {
+  if (threadIdx.x < T) dst[threadIdx.x] = r0 + threadIdx.x < end ? src[r0 + threadIdx.x] : pad;
+}
+
+// dQ of a query tile
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                      const float* __restrict__ dout, const float* __restrict__ lse, const float* __restrict__ delta,
+                      const Window w, int group, float scale, float* __restrict__ dq) {
+  constexpr int P = padded<D>();
+  extern __shared__ __align__(16) float sm[];
+  float *Q = sm, *O = Q + T * P, *K = O + T * P, *V = K + T * P, *W = V + T * P, *ls = W + T * SP, *de = ls + T;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tiles = ceil_div(w.Nq, T), bh = blockIdx.x / tiles, q0 = (blockIdx.x - bh * tiles) * T;
+  const int q1 = min(q0 + T, w.Nq);
+  const size_t qh = (size_t)bh * w.Nq * D, kh = (size_t)(bh / group) * w.Nk * D;
+  stage<D>(Q, q + qh, q0, w.Nq);
+  stage<D>(O, dout + qh, q0, w.Nq);
+  stage_vec(ls, lse + (size_t)bh * w.Nq, q0, w.Nq, -INFINITY);
+  stage_vec(de, delta + (size_t)bh * w.Nq, q0, w.Nq, 0.f);
+  float acc[4][D / 16] = {};
+  const KeyTiles<T> kt = KeyTiles<T>::of(w, q0, q1);
+  for (int e = 0; e < kt.count(); ++e) {
+    const int k0 = kt.tile(e) * T;
+    __syncthreads();
+    stage<D>(K, k + kh, k0, w.Nk);
+    stage<D>(V, v + kh, k0, w.Nk);
+    __syncthreads();
+    float s[4][4] = {}, dp[4][4] = {}, p[4][4], ds[4][4];
+    product_nt<D>(s, Q, K, ty, tx);
+    product_nt<D>(dp, O, V, ty, tx);
+    weights(s, dp, p, ds, w, q0, k0, all_visible(w, q0, q1, k0, k0 + T), scale, ls, de, ty, tx);
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) W[(ty + 16 * a) * SP + tx + 16 * b] = ds[a][b];
+    __syncthreads();
+    product_nn<D>(acc, W, K, ty, tx);
+  }
+  float mul[4] = {scale, scale, scale, scale};
+  store_rows<D>(dq + qh, acc, q0, q1, mul, ty, tx);
+}
+
+// dK and dV of a key tile, over the query heads of its key head
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                        const float* __restrict__ dout, const float* __restrict__ lse,
+                        const float* __restrict__ delta, const Window w, int group, float scale,
+                        float* __restrict__ dk, float* __restrict__ dv) {
+  constexpr int P = padded<D>();
+  extern __shared__ __align__(16) float sm[];
+  float *K = sm, *V = K + T * P, *Q = V + T * P, *O = Q + T * P, *W = O + T * P, *ls = W + T * SP, *de = ls + T;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tiles = ceil_div(w.Nk, T), kv = blockIdx.x / tiles, k0 = (blockIdx.x - kv * tiles) * T;
+  const int k1 = min(k0 + T, w.Nk);
+  const size_t kh = (size_t)kv * w.Nk * D;
+  stage<D>(K, k + kh, k0, w.Nk);
+  stage<D>(V, v + kh, k0, w.Nk);
+  float ak[4][D / 16] = {}, av[4][D / 16] = {};
+  const QueryRun run = QueryRun::of(w, k0, k1);
+  for (int h = 0; h < group; ++h) {
+    const size_t bh = (size_t)kv * group + h, qh = bh * w.Nq * D;
+    for (int q0 = run.q0 / T * T; q0 < run.q1; q0 += T) {
+      __syncthreads();
+      stage<D>(Q, q + qh, q0, w.Nq);
+      stage<D>(O, dout + qh, q0, w.Nq);
+      stage_vec(ls, lse + bh * w.Nq, q0, w.Nq, -INFINITY);
+      stage_vec(de, delta + bh * w.Nq, q0, w.Nq, 0.f);
+      __syncthreads();
+      float s[4][4] = {}, dp[4][4] = {}, p[4][4], ds[4][4];
+      product_nt<D>(s, Q, K, ty, tx);
+      product_nt<D>(dp, O, V, ty, tx);
+      weights(s, dp, p, ds, w, q0, k0, all_visible(w, q0, min(q0 + T, w.Nq), k0, k0 + T), scale, ls, de, ty, tx);
+      // transposed into shared memory: row = key
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = p[a][b];
+      __syncthreads();
+      product_nn<D>(av, W, O, ty, tx);
+      __syncthreads();
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = ds[a][b];
+      __syncthreads();
+      product_nn<D>(ak, W, Q, ty, tx);
+    }
+  }
+  float one[4] = {1.f, 1.f, 1.f, 1.f}, mul[4] = {scale, scale, scale, scale};
+  store_rows<D>(dv + kh, av, k0, k1, one, ty, tx);
+  store_rows<D>(dk + kh, ak, k0, k1, mul, ty, tx);
+}
+
+template <int D>
+cudaError_t fwd_d(const WindowAttn& a, cudaStream_t s) {
+  const size_t smem = (2 * T * padded<D>() + T * SP) * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(window_fwd_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  window_fwd_simt_kernel<D><<<a.B * a.H * ceil_div(a.w.Nq, T), kThreads, smem, s>>>(
+      static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), a.w, a.H / a.Hk,
+      a.scale, static_cast<float*>(a.out), a.lse);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t bwd_d(const WindowAttn& a, cudaStream_t s) {
+  const size_t smem = (4 * T * padded<D>() + T * SP + 2 * T) * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(window_dq_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(window_dkdv_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const float *q = static_cast<const float*>(a.q), *k = static_cast<const float*>(a.k),
+              *v = static_cast<const float*>(a.v), *g = static_cast<const float*>(a.dout);
+  const int group = a.H / a.Hk;
+  window_dq_simt_kernel<D><<<a.B * a.H * ceil_div(a.w.Nq, T), kThreads, smem, s>>>(
+      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, static_cast<float*>(a.dq));
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  window_dkdv_simt_kernel<D><<<a.B * a.Hk * ceil_div(a.w.Nk, T), kThreads, smem, s>>>(
+      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, static_cast<float*>(a.dk), static_cast<float*>(a.dv));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_simt(const WindowAttn& a, cudaStream_t s) {
+  return a.D == 64 ? fwd_d<64>(a, s) : fwd_d<128>(a, s);
+}
+
+cudaError_t launch_window_bwd_simt(const WindowAttn& a, cudaStream_t s) {
+  return a.D == 64 ? bwd_d<64>(a, s) : bwd_d<128>(a, s);
+}
+
+}  // namespace dsa

@@ -547,6 +547,114 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, xq, xk, wq: Optional[to
     return dxq, dxk, dwq, dwk
 
 
+def _check_window(q, k, v, out=None, dout=None):
+    """B, H, Hk, Nq, Nk, D of q [B, H, Nq, D] and k, v [B, Hk, Nk, D]."""
+    for t in (q, k, v):
+        if t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("q, k, v must be contiguous CUDA tensors [B, H, N, D]")
+        if t.dtype != q.dtype or t.device != q.device or t.shape[0] != q.shape[0] or t.shape[3] != q.shape[3]:
+            raise ValueError("q, k, v must share B, D, dtype and device")
+    if k.shape != v.shape:
+        raise ValueError("k and v must share their shape")
+    for t in (out, dout):
+        if t is not None and (t.shape != q.shape or t.dtype != q.dtype or t.device != q.device
+                              or not t.is_contiguous()):
+            raise ValueError("out and dout must match q")
+    B, H, Nq, D = q.shape
+    return B, H, k.shape[1], Nq, k.shape[2], D
+
+
+def _check_lse(lse, q):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != q.device
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [B, H, Nq] on q's device")
+
+
+def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int = -1, right: int = 0,
+                    sink: int = 0, q_offset: Optional[int] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    want_lse: bool = True):
+    """(O [B, H, Nq, D], lse [B, H, Nq] or None): softmax attention in which key
+    u is visible to the query at position t = q_offset + i iff u <= t + right
+    and (u < sink or u >= t - left); a negative bound is no bound.
+
+    q [B, H, Nq, D], k and v [B, Hk, Nk, D] with Hk dividing H.  q_offset
+    defaults to Nk - Nq: the queries are the newest tokens."""
+    B, H, Hk, Nq, Nk, D = _check_window(q, k, v, out)
+    _check_lse(lse, q)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty_like(q)
+    if want_lse and lse is None:
+        lse = torch.empty(B, H, Nq, device=q.device, dtype=torch.float32)
+    with torch.cuda.device(q.device):
+        st = lib().dsa_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hk, Nq,
+                                       Nk, D, scale, Nk - Nq if q_offset is None else int(q_offset),
+                                       int(left), int(right), int(sink), out.data_ptr(), _ptr(lse), _stream(q))
+    check(st, "dsa_window_attn_fwd")
+    return out, lse
+
+
+def window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                    dout: torch.Tensor, lse: torch.Tensor, left: int = -1, right: int = 0, sink: int = 0,
+                    q_offset: Optional[int] = None, scale: Optional[float] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """(dQ, dK, dV) of window_attn_fwd's O for its gradient dout, with the O and
+    lse it gave and the same mask; dK and dV summed over shared heads."""
+    B, H, Hk, Nq, Nk, D = _check_window(q, k, v, out, dout)
+    if lse is None:
+        raise ValueError("the forward's lse is required")
+    _check_lse(lse, q)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    if workspace is None:
+        n = int(lib().dsa_window_attn_bwd_workspace_size(B, H, Nq))
+        workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+    with torch.cuda.device(q.device):
+        st = lib().dsa_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                       dout.data_ptr(), lse.data_ptr(), _dtype_code(q), B, H, Hk, Nq, Nk, D,
+                                       scale, Nk - Nq if q_offset is None else int(q_offset), int(left),
+                                       int(right), int(sink), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                       _stream(q))
+    check(st, "dsa_window_attn_bwd")
+    return dq, dk, dv
+
+
+def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
+                       left: int = -1, sink: int = 0, scale: Optional[float] = None,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """O [B, H, Nq, D] of each stream's newest Nq tokens (up to 128) over its
+    cache: window_attn_fwd with right = 0 and q_offset = lens[b] - Nq.
+
+    k_cache, v_cache [B, Hk, cap, D] may be strided (rows of D contiguous);
+    lens int32 [B] on the device counts the keys in each cache, the new tokens'
+    among them.  lse, if given, receives the log-sums [B, H, Nq]."""
+    if q.dim() != 4 or not q.is_cuda or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA tensor [B, H, Nq, D]")
+    B, H, Nq, D = q.shape
+    for t in (k_cache, v_cache):
+        if t.dim() != 4 or t.dtype != q.dtype or t.device != q.device or t.shape != k_cache.shape \
+                or t.shape[0] != B or t.shape[3] != D or t.stride(3) != 1:
+            raise ValueError("caches must be [B, Hk, cap, D] of q's dtype and device with contiguous rows")
+    if lens.dtype != torch.int32 or lens.device != q.device or lens.shape != (B,) or not lens.is_contiguous():
+        raise ValueError("lens must be contiguous int32 [B] on q's device")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must match q")
+    _check_lse(lse, q)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    st6 = _strides6(*([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k_cache, v_cache)))
+    with torch.cuda.device(q.device):
+        st = lib().dsa_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), st6.data_ptr(),
+                                          _dtype_code(q), B, H, k_cache.shape[1], Nq, k_cache.shape[2], D,
+                                          scale, lens.data_ptr(), int(left), int(sink), out.data_ptr(),
+                                          _ptr(lse), _stream(q))
+    check(st, "dsa_window_attn_decode")
+    return out
+
+
 def selftest_wait_timeout(limit_ns: int = 1_000_000, device: Optional[torch.device] = None) -> None:
     """Launch the failure-detection self-test: a bounded wait that runs out
     after limit_ns and records a wait timeout (dsa_device_status then raises)."""

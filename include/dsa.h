@@ -525,6 +525,85 @@ dsa_status dsa_qk_norm_rope_bwd(const void* dq, const void* dk, const void* xq, 
 size_t dsa_qk_norm_rope_bwd_workspace_size(int D);
 
 /*
+ * Attention with a local window and first tokens that stay visible.  (No
+ * counterpart in the papers beyond their baseline of fixed masks: a window
+ * over neighbouring frames, or over neighbours along a Hilbert order, with
+ * the text prefix in sight; causal, it is the mask of streamed generation.)
+ *
+ * Query i stands at position t = q_offset + i, key u at position u.  Key u is
+ * visible to it iff
+ *   u <= t + right  and  (u < sink or u >= t - left).
+ * The right bound holds for the first `sink` keys too (right = 0 is causal
+ * throughout); a negative left or right bounds nothing.
+ *
+ *   o_i = sum over the visible u of softmax_u(scale q_i . k_u) v_u
+ *
+ *   q         [B, H, Nq, D] in dt;  k, v  [B, Hk, Nk, D]; H a multiple of Hk:
+ *             query head h reads key head h / (H / Hk).
+ *   out       [B, H, Nq, D] in dt.
+ *   lse       optional out, fp32 [B, H, Nq]: natural-log sum of exp(scale q.k)
+ *             over the visible keys.
+ * A query that sees no key gets o = 0 and lse = -inf.  What k holds in hidden
+ * places does not matter; a NaN or an infinity in v reaches the queries of
+ * every tile that loads its row (0 * NaN), as in a dense masked product.
+ * bf16 runs on tcgen05 tensor cores with fp32 accumulation (weights rounded
+ * to bf16 for the second product), fp32 in exact fp32 on CUDA cores.
+ * Limits: D 64 or 128; B*H <= 65535; Nq, Nk 1 .. 2^27; |q_offset| <= 2^28;
+ * sink >= 0.  All tensors contiguous and 16-byte aligned.
+ */
+dsa_status dsa_window_attn_fwd(const void* q, const void* k, const void* v, dsa_dtype dt, int B,
+                               int H, int Hk, int Nq, int Nk, int D, float scale, int q_offset,
+                               int left, int right, int sink, void* out, float* lse,
+                               void* stream);
+
+/*
+ * Gradients of dsa_window_attn_fwd's o.  With P the softmax of each query over
+ * its visible keys (from lse), dP = dO V^T and delta = rowsum(dO * O):
+ *   dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+ * dK and dV summed over the query heads that share a key head.
+ *
+ *   out, lse   the forward's (lse is required);  dout  [B, H, Nq, D] in dt.
+ *   dq         out, [B, H, Nq, D];  dk, dv  out, [B, Hk, Nk, D], in dt.  Keys
+ *              that no query sees get 0, queries that see no key get dQ = 0.
+ *   workspace  >= dsa_window_attn_bwd_workspace_size(B, H, Nq) bytes, 16-byte
+ *              aligned.
+ * Every sum has a fixed order: two calls give the same bits.  bf16 runs on
+ * tcgen05 with dS as two bf16 terms and P as one; fp32 in exact fp32.
+ * Limits as for the forward.
+ */
+dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                               const void* dout, const float* lse, dsa_dtype dt, int B, int H,
+                               int Hk, int Nq, int Nk, int D, float scale, int q_offset, int left,
+                               int right, int sink, void* dq, void* dk, void* dv, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/* Device workspace bytes for dsa_window_attn_bwd; 0 for invalid sizes. */
+size_t dsa_window_attn_bwd_workspace_size(int B, int H, int Nq);
+
+/*
+ * The causal window attention (right = 0) of the newest Nq tokens of each
+ * stream over its cache of keys and values.
+ *
+ *   q         [B, H, Nq, D] in dt, contiguous;  Nq 1 .. 128.
+ *   k, v      caches [B, Hk, cap, D] in dt, read through `kv_strides` (host,
+ *             int64 [6]: k's strides of b, h, n, then v's, in elements; D
+ *             contiguous, strides multiples of 16 bytes).
+ *   lens      device, int32 [B]: the keys in each stream's cache, the Nq new
+ *             ones among them; query i stands at position lens[b] - Nq + i.
+ *             A query at a negative position sees nothing (o = 0, lse = -inf).
+ *   left, sink, out, lse  as in dsa_window_attn_fwd.
+ * Cache rows that no query sees are not read.  One launch, no workspace; lens
+ * is read on the device, so a captured call serves a growing cache.
+ * Errors: DSA_ERR_INVALID_ARG as listed; a length outside [0, cap] sets the
+ * device error word and is taken as 0.
+ * Limits: D 64 or 128; B*H <= 65535; cap 1 .. 2^27; sink >= 0.
+ */
+dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
+                                  const int64_t* kv_strides, dsa_dtype dt, int B, int H, int Hk,
+                                  int Nq, int cap, int D, float scale, const int32_t* lens,
+                                  int left, int sink, void* out, float* lse, void* stream);
+
+/*
  * Activation rows kept in 8 bits between the forward and the backward.  (No
  * counterpart in the papers; DSV's abstract trains at 520k tokens, where the
  * activations kept for the backward are what fills the memory.)
