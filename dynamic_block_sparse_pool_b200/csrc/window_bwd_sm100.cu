@@ -170,7 +170,6 @@ template <int D, typename Grads>
 __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, unsigned* err) {
   using L = Smem<D>;
   constexpr uint32_t kTileBytes = L::kTile;
-  const bool leader = c.lane == 0;
   const uint64_t dA = smem_desc_sw128(c.base + L::kFixA, 16, 1024), dB = smem_desc_sw128(c.base + L::kFixB, 16, 1024);
   const uint64_t da = smem_desc_sw128(c.base + L::kRingA, 16, 1024), db = smem_desc_sw128(c.base + L::kRingB, 16, 1024);
   bool ok = warp_all(mbar_wait(c.bar(kBarFixed), 0u));
@@ -178,7 +177,7 @@ __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, uns
     const int s = it & 1;
     if (h == 0 && !(ok = ok && warp_all(mbar_wait(c.bar(kBarRing + s), (uint32_t)(it >> 1) & 1u)))) return;
     tc_fence_after();
-    if (leader) {
+    if (elect_one()) {
       const uint64_t off = (uint64_t)((s * kTileBytes) >> 4);
       mma_rows_half<D>(c.tmem + kColS + 64 * h, dA, da + off, h);
       mma_rows_half<D>(c.tmem + kColP + 64 * h, dB, db + off, h);
@@ -193,7 +192,7 @@ __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, uns
     for (int h = 0; h < 2 && ok; ++h) {
       if (!(ok = warp_all(mbar_wait(c.bar(kBarP + h), (uint32_t)it & 1u)))) break;
       tc_fence_after();
-      if (leader) {
+      if (elect_one()) {
         grads(h, (uint64_t)((s * kTileBytes) >> 4), it > 0 || h > 0);
         if (h == 1) mma_commit(c.bar(kBarFree + s));
       }

@@ -5,8 +5,8 @@
 // For every query: softmax over its visible keys (window.cuh), in one pass
 // over key tiles of 128 with a running reference m and sum l:
 //   P = 2^(S scale log2e - m),  l += rowsum(P),  O += P V;  O / l at the end.
-// m only moves when a tile's maximum exceeds it by more than 8 (base 2), and
-// then l and O are rescaled: P stays below 2^8, where bf16 and fp32 are as
+// m only moves when a tile's maximum exceeds it by more than 16 (base 2), and
+// then l and O are rescaled: P stays below 2^16, where bf16 and fp32 are as
 // precise as below 1, and O and l share the reference, so the result is the
 // softmax all the same.  P is rounded to bf16 for the second product (at most
 // half a step, 2^-9 of each weight; l sums the unrounded values).
@@ -19,17 +19,20 @@
 // overlapping windows, which L2 holds).  384 threads:
 //   warps 0-3  softmax and output of query tile A, one row per thread
 //   warps 4-7  the same for tile B
-//   warp  8    MMA issuer (and tensor-memory allocation)
-//   warp  9    TMA loader: the two Q tiles, then K and V tiles through a ring
-//   (warps 10 and 11 only complete the warpgroup that gives registers up)
+//   warps 8, 9 MMA issuers of tile A and tile B (8 also allocates tensor
+//              memory): an MMA and a wait cost an issuer as many cycles as the
+//              tensor cores take for them, so each tile has its own
+//   warp  10   TMA loader: the two Q tiles, then K and V tiles through a ring
+//   (warp 11 only completes the warpgroup that gives registers up)
 // Tensor memory: S_A, S_B (128 columns each; P overwrites S in place as
 // packed bf16), O_A, O_B.  While tile A is in its softmax the tensor cores
 // run tile B's PV and next S, and the other way round.  The MMAs of one
 // thread run in order, so S(i+1) overwrites the buffer of P(i) after PV(i)
 // has read it, and a finished S(i+1) also means that PV(i) is done: the
-// softmax warps may rescale O, and after the last PV read it out, without
-// another barrier; the next item's first PV waits for their P, which they
-// write after they have read O.
+// softmax warps may rescale O.  The last PV has a barrier of its own (the
+// next item's first S may be done before every softmax warp has noticed, and
+// one barrier for both would run a phase ahead of it); the next item's first
+// PV waits for their P, which they write after they have read O out.
 //
 // Masks: a key tile that every row of the query tile sees in full needs
 // none; in the others hidden scores become -inf before the maximum, so what
@@ -53,15 +56,10 @@ constexpr int kThreads = 384;
 // warps, which hold a row of S, take 208, the others keep 88 (256 * 208 +
 // 128 * 88 = 64,512).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;  // MMA issuers: 8 (tile A), 9 (tile B)
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kStep = 8.f;  // the reference moves when a maximum exceeds it by more
-
-// Pairs of the 16 in each chunk of 32 keys whose exponentials run on the FMA
-// pipe instead of the MUFU.
-template <int D>
-constexpr int poly_pairs() { return 0; }
+constexpr float kStep = 16.f;  // the reference moves when a maximum exceeds it by more
 
 template <int D>
 struct Smem {
@@ -71,10 +69,11 @@ struct Smem {
   static constexpr int kQ = 0;                    // two tiles
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBar = kRing + kStages * kTile;
-  // barriers: Q landed, Q free, ring landed / free, S (or the last PV) done
-  // per query tile, P written per query tile and half
-  static constexpr int kQFull = 0, kQFree = 1, kFull = 2, kFree = kFull + kStages,
-                       kS = kFree + kStages, kP = kS + 2, kDrain = kP + 4, kNumBars = kDrain + 1;
+  // barriers: per query tile Q landed, Q free; ring landed / free; per query
+  // tile S done, its last PV done, and (by half) P written; teardown
+  static constexpr int kQFull = 0, kQFree = 2, kFull = 4, kFree = kFull + kStages,
+                       kS = kFree + kStages, kO = kS + 2, kP = kO + 2, kDrain = kP + 4,
+                       kNumBars = kDrain + 2;
   static constexpr int kSlot = kBar + 8 * kNumBars;
   static constexpr int kBytes = kSlot + 16;
 };
@@ -140,7 +139,12 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
   if (warp == kMmaWarp) {
     if (lane == 0) {
-      for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i >= L::kP && i < L::kP + 4 ? 4u : 1u);
+      for (int i = 0; i < L::kNumBars; ++i) {
+        uint32_t count = 1;
+        if (i >= L::kP && i < L::kP + 4) count = 4;                          // softmax warps
+        if (i >= L::kFree && i < L::kFree + ST) count = 2;   // MMA issuers
+        mbar_init(bar(i), count);
+      }
       *abort_flag = 0;
       fence_mbar_init();
     }
@@ -157,133 +161,162 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  uint32_t issued = 0, q_issued = 0;  // loader: ring tiles and Q loads issued
+  uint32_t issued = 0, q_issued = 0;  // loader: ring tiles issued, items whose Q tiles are
+  int q_last = -1;                    // the query tile whose Q was loaded last
   bool had_mma = false;
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------------ loader
-    if (lane == 0) {
-      bool ok = true;
-      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-        const Item it(p, i);
-        const int n = it.all.count();
-        if (n == 0) continue;
-        // Q's buffer is free once every S of the previous item is done
-        if (q_issued > 0 && !(ok = mbar_wait(bar(L::kQFree), (q_issued - 1) & 1u) && !*abort_flag)) break;
-        const bool two = it.b.count() > 0;
-        mbar_expect_tx(bar(L::kQFull), two ? 2 * kTileBytes : kTileBytes);
-        load_tile<D>(base + L::kQ, &tmQ, it.q0, it.bh, bar(L::kQFull));
-        if (two) load_tile<D>(base + L::kQ + kTileBytes, &tmQ, it.q0 + BM, it.bh, bar(L::kQFull));
-        ++q_issued;
-        // K(0), then K(e), V(e - 1) in the order the MMA issuer takes them
-        for (int e = 0; e <= 2 * n - 1 && ok; ++e) {
-          const bool is_k = e == 0 || ((e & 1) && e < 2 * n - 1);
-          const int blk = is_k ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1;
-          const uint32_t s = issued % ST;
-          if (!(ok = mbar_wait(bar(L::kFree + s), ((issued / ST) & 1u) ^ 1u) && !*abort_flag)) break;
-          mbar_expect_tx(bar(L::kFull + s), kTileBytes);
-          load_tile<D>(base + L::kRing + s * kTileBytes, is_k ? &tmK : &tmV, it.all.tile(blk) * BN, it.kv,
-                       bar(L::kFull + s));
-          ++issued;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------------ loader
+      if (lane == 0) {
+        bool ok = true;
+        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+          const Item it(p, i);
+          const int n = it.all.count();
+          if (n == 0) continue;
+          // Q's buffers are free once the last S of the tile's previous item is
+          // done; K(0) goes between them, so tile A need not wait for tile B
+          auto load_q = [&](int x) {
+            ok = ok && (q_issued == 0 || mbar_wait(bar(L::kQFree + x), (q_issued - 1) & 1u)) && !*abort_flag;
+            if (!ok) return;
+            mbar_expect_tx(bar(L::kQFull + x), kTileBytes);
+            // a second tile behind the last query reads as zeros
+            load_tile<D>(base + L::kQ + x * kTileBytes, &tmQ, it.q0 + BM * x, it.bh, bar(L::kQFull + x));
+            q_last = x;
+          };
+          // K(0), then K(e), V(e - 1) in the order the MMA issuers take them
+          load_q(0);
+          for (int e = 0; e <= 2 * n - 1 && ok; ++e) {
+            if (e == 1) {
+              load_q(1);
+              if (!ok) break;
+              ++q_issued;
+            }
+            const bool is_k = e == 0 || ((e & 1) && e < 2 * n - 1);
+            const int blk = is_k ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1;
+            const uint32_t s = issued % ST;
+            if (!(ok = mbar_wait(bar(L::kFree + s), ((issued / ST) & 1u) ^ 1u) && !*abort_flag)) break;
+            mbar_expect_tx(bar(L::kFull + s), kTileBytes);
+            load_tile<D>(base + L::kRing + s * kTileBytes, is_k ? &tmK : &tmV, it.all.tile(blk) * BN, it.kv,
+                         bar(L::kFull + s));
+            ++issued;
+          }
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          flag_error(err, kErrTimeout);
         }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        flag_error(err, kErrTimeout);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // -------------------------------------------------------------- MMA issuer
-    const bool leader = lane == 0;
-    constexpr uint32_t kIdescS = idesc_bf16_f32(BM, BN, false);
-    constexpr uint32_t kIdescO = idesc_bf16_f32(BM, D, true);
-    const uint64_t dq = smem_desc_sw128(base + L::kQ, 16, 1024);
-    const uint64_t dk = smem_desc_sw128(base + L::kRing, 16, 1024);
-    const uint64_t dv = smem_desc_sw128(base + L::kRing, L::kSub, 1024);
-    auto kstep = [](int kk) -> uint64_t {  // 16 columns of D in a K-major tile
-      return (uint64_t)(((kk >> 2) * L::kSub + (kk & 3) * 32) >> 4);
-    };
-    uint32_t pos = 0;                   // ring tiles taken so far
-    uint32_t p_seen[2] = {0u, 0u};      // P tiles taken of each query tile
-    uint32_t q_seen = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-      const Item it(p, i);
-      const int n = it.all.count();
-      if (n == 0) continue;
-      if (!(ok = warp_all(mbar_wait(bar(L::kQFull), q_seen & 1u)))) break;
-      ++q_seen;
-      had_mma = true;
-      // the last key tile of each query tile (-1: none)
-      int last_a = n - 1, last_b = n - 1;
-      while (last_a >= 0 && !it.a.has(it.all.tile(last_a))) --last_a;
-      while (last_b >= 0 && !it.b.has(it.all.tile(last_b))) --last_b;
-      bool pend[2] = {false, false}, started[2] = {false, false};
-      for (int e = 0; e <= n && ok; ++e) {
-        const int j = e < n ? it.all.tile(e) : -1;
-        // ring order: K(0), K(1), V(0), K(2), V(1), ..., V(n - 1)
-        const uint32_t k_at = e == 0 ? pos : pos + 2 * e - 1;
-        const uint32_t v_at = e == n ? pos + 2 * n - 1 : pos + 2 * e;  // V(e - 1), e >= 1
-        const uint32_t ks = k_at % ST, vs = v_at % ST;
-        if (e < n && !(ok = warp_all(mbar_wait(bar(L::kFull + ks), (k_at / ST) & 1u)))) break;
-        bool v_here = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t tS = tmem + 128u * x, tO = tmem + kColO + (uint32_t)D * x;
-          const bool act = e < n && (x ? it.b : it.a).has(j);
-          if (!act && !pend[x]) continue;
-          if (pend[x]) {
-            // O (+)= P(e - 1) V(e - 1), a half of the keys at a time
-            if (!v_here && !(ok = warp_all(mbar_wait(bar(L::kFull + vs), (v_at / ST) & 1u)))) break;
-            v_here = true;
-            const uint64_t v0 = dv + (uint64_t)((vs * kTileBytes) >> 4);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ------------------------------------------------------------- MMA issuers
+      // One warp per query tile.  The whole warp runs the loop on values that
+      // every lane knows to be the same (broadcasts, votes), so descriptors and
+      // addresses are computed once per warp in uniform registers; one
+      // elected lane issues the MMAs and commits.
+      const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+      constexpr uint32_t kIdescS = idesc_bf16_f32(BM, BN, false);
+      constexpr uint32_t kIdescO = idesc_bf16_f32(BM, D, true);
+      const uint32_t ubase = __shfl_sync(0xffffffffu, base, 0), utmem = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t tS = utmem + 128u * x, tO = utmem + kColO + (uint32_t)D * x;
+      const uint64_t dq = smem_desc_sw128(ubase + L::kQ + x * kTileBytes, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(ubase + L::kRing, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(ubase + L::kRing, L::kSub, 1024);
+      const uint32_t ubars = ubase + L::kBar;
+      auto ubar = [&](int i) { return ubars + 8u * (uint32_t)i; };
+      auto kstep = [](int kk) -> uint64_t {  // 16 columns of D in a K-major tile
+        return (uint64_t)(((kk >> 2) * L::kSub + (kk & 3) * 32) >> 4);
+      };
+      uint32_t ring = 0, ring_ph = 0;  // the next ring tile's stage and phase
+      uint32_t p_ph = 0, q_ph = 0;     // phases of the next P tile and Q load
+      bool ok = true;
+      auto advance = [&](uint32_t& st, uint32_t& ph, uint32_t by) {
+        st += by;
+        if (st >= ST) {
+          st -= ST;
+          ph ^= 1u;
+        }
+      };
+      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        const Item it(p, i);
+        const int n = __shfl_sync(0xffffffffu, it.all.count(), 0);
+        if (n == 0) continue;
+        // key tile positions e at which this query tile is active: two runs
+        const KeyTiles<BN> mine = x ? it.b : it.a;
+        const int f = __shfl_sync(0xffffffffu, min(mine.first, n), 0);
+        const int r0 = __shfl_sync(0xffffffffu, mine.begin - it.all.begin + it.all.first, 0);
+        const int r1 = __shfl_sync(0xffffffffu, mine.end - it.all.begin + it.all.first, 0);
+        const int first = f > 0 ? 0 : r0, last = (r1 > r0 ? r1 : f) - 1;
+        if (!(ok = warp_all(mbar_wait(ubar(L::kQFull + x), q_ph)))) break;
+        q_ph ^= 1u;
+        had_mma = true;
+        uint32_t ks = ring, kph = ring_ph;  // K(e)
+        uint32_t vs = ring, vph = ring_ph;  // V(e - 1)
+        bool pend = false;                  // P(e - 1) is on its way
+        // ring order: K(0), K(1), V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1)
+        for (int e = 0; e <= n; ++e) {
+          if (e == 1) {
+            advance(ks, kph, 1);
+            advance(vs, vph, n == 1 ? 1 : 2);
+          } else if (e > 1) {
+            advance(ks, kph, 2);
+            advance(vs, vph, e == n ? 1 : 2);
+          }
+          if (e < n && !(ok = warp_all(mbar_wait(ubar(L::kFull + ks), kph)))) break;
+          if (e > 0 && !(ok = warp_all(mbar_wait(ubar(L::kFull + vs), vph)))) break;
+          const uint64_t k0 = dk + (uint64_t)(ks * (kTileBytes >> 4)), v0 = dv + (uint64_t)(vs * (kTileBytes >> 4));
+          const bool act = e < n && (e < f || (e >= r0 && e < r1));
+          if (pend) {
+            // O (+)= P(e - 1) V(e - 1), a half of the keys at a time; the tile's
+            // first PV overwrites O
+            const uint32_t more = e - 1 > first;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (!(ok = ok && warp_all(mbar_wait(bar(L::kP + 2 * x + h), p_seen[x] & 1u)))) break;
+              if (!(ok = ok && warp_all(mbar_wait(ubar(L::kP + 2 * x + h), p_ph)))) break;
               tc_fence_after();
-              if (leader) {
+              if (elect_one()) {
 #pragma unroll
                 for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                  mma_ts(tO, tS + 8u * kk, v0 + (uint64_t)((kk * 2048) >> 4), kIdescO,
-                         started[x] || kk > 0 ? 1u : 0u);
+                  mma_ts(tO, tS + 8u * kk, v0 + (uint64_t)((kk * 2048) >> 4), kIdescO, kk > 0 ? 1u : more);
               }
               __syncwarp();
             }
             if (!ok) break;
-            ++p_seen[x];
-            started[x] = true;
-            pend[x] = false;
+            p_ph ^= 1u;
           }
           if (act) {
-            if (leader) {
-              const uint64_t k0 = dk + (uint64_t)((ks * kTileBytes) >> 4);
-              const uint64_t q0 = dq + (uint64_t)((x * kTileBytes) >> 4);
-              mma_ss(tS, q0, k0, kIdescS, 0u);
+            if (elect_one()) {
 #pragma unroll
-              for (int kk = 1; kk < D / 16; ++kk) mma_ss_acc(tS, q0 + kstep(kk), k0 + kstep(kk), kIdescS);
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tS, dq + kstep(kk), k0 + kstep(kk), kIdescS, kk > 0 ? 1u : 0u);
             }
-            pend[x] = true;
+            __syncwarp();
           }
-          // S(e) is done, or the tile's last PV
-          if (leader && (act || e > (x ? last_b : last_a))) mma_commit(bar(L::kS + x));
+          // S(e) is done; the tile's last PV has its own barrier: the next
+          // item's first S may follow before every softmax warp has seen it
+          if (act) {
+            if (elect_one()) mma_commit(ubar(L::kS + x));
+          } else if (pend && e > last) {
+            if (elect_one()) mma_commit(ubar(L::kO + x));
+          }
+          pend = act;
+          // (with the other tile's issuer: two arrivals free a tile)
+          if (elect_one()) {
+            if (e > 0) mma_commit(ubar(L::kFree + vs));
+            if (e < n) mma_commit(ubar(L::kFree + ks));
+            if (e == n - 1) mma_commit(ubar(L::kQFree + x));
+          }
           __syncwarp();
         }
-        if (!ok) break;
-        if (leader) {
-          if (e < n) mma_commit(bar(L::kFree + ks));
-          if (e > 0) mma_commit(bar(L::kFree + vs));
-          if (e == n - 1) mma_commit(bar(L::kQFree));
-        }
-        __syncwarp();
+        // the next item's K(0) follows V(n - 1)
+        ring = vs;
+        ring_ph = vph;
+        advance(ring, ring_ph, 1);
       }
-      pos += 2 * n;
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        flag_error(err, kErrTimeout);
+      }
     }
-    if (!ok && leader) {
-      *abort_flag = 1;
-      flag_error(err, kErrTimeout);
-    }
-  }
   } else {
     // ----------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -292,7 +325,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lane_off + 128u * x, tO = tmem + lane_off + kColO + (uint32_t)D * x;
     const float scale = p.scale_log2;
-    uint32_t seen = 0;  // phases of S done taken so far
+    uint32_t seen = 0, o_ph = 0;  // phases of S taken so far, phase of the next complete O
     bool ok = true;
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
       const Item it(p, i);
@@ -340,15 +373,15 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (move) mref = m;
           l *= alpha;
           if (e > 0) {
-            // O holds the sum through the previous key tile
+            // O holds the sum through the previous key tile (16 columns at a
+            // time: the row of S stays in registers meanwhile)
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16_wait(tO + 16 * c, o);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + 32 * c, o);
-              tmem_wait_ld_regs(o);
-#pragma unroll
-              for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-              tmem_st32(tO + 32 * c, o);
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+              tmem_st16(tO + 16 * c, o);
             }
           }
         }
@@ -360,18 +393,12 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           uint32_t pk[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(s[c][2 * u]), __uint_as_float(s[c][2 * u + 1])),
-                                   sc2, nm2);
-            if ((u + 1) * poly_pairs<D>() / 16 != u * poly_pairs<D>() / 16) {
-              y = exp2_poly_x2(y);
-            } else {
-              float a, b;
-              unpack_f32x2(y, a, b);
-              y = pack_f32x2(exp2_mufu(a), exp2_mufu(b));
-            }
-            sum2[u & 1] = add_f32x2(sum2[u & 1], y);
             float a, b;
-            unpack_f32x2(y, a, b);
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[c][2 * u]), __uint_as_float(s[c][2 * u + 1])), sc2, nm2),
+                         a, b);
+            a = exp2_mufu(a);
+            b = exp2_mufu(b);
+            sum2[u & 1] = add_f32x2(sum2[u & 1], pack_f32x2(a, b));
             const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
             pk[u] = *reinterpret_cast<const uint32_t*>(&h2);
           }
@@ -388,10 +415,9 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         l += a + b;
       }
       if (!ok) break;
-      // O is complete with the next phase of S done
-      if (n > 0) {
-        if (!(ok = warp_all(mbar_wait(bar(L::kS + x), seen & 1u)))) break;
-        ++seen;
+      if (n > 0) {  // O is complete
+        if (!(ok = warp_all(mbar_wait(bar(L::kO + x), o_ph)))) break;
+        o_ph ^= 1u;
         tc_fence_after();
       }
       const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
@@ -431,16 +457,19 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   if (*abort_flag) {
     // A role gave up: let every copy and MMA in flight finish (bounded)
     // before shared and tensor memory are released.
-    if (warp == kMmaWarp && had_mma) {
+    if (had_mma) {  // the MMA issuers
       if (lane == 0) {
-        mma_commit(bar(L::kDrain));
-        mbar_wait(bar(L::kDrain), 0u);
+        mma_commit(bar(L::kDrain + warp - kMmaWarp));
+        mbar_wait(bar(L::kDrain + warp - kMmaWarp), 0u);
       }
       __syncwarp();
     } else if (warp == kLoadWarp && lane == 0) {
       for (uint32_t b = issued > ST ? issued - ST : 0; b < issued; ++b)
         mbar_wait(bar(L::kFull + b % ST), (b / ST) & 1u);
-      if (q_issued > 0) mbar_wait(bar(L::kQFull), (q_issued - 1) & 1u);
+      // (tile A is one load ahead of tile B between the two)
+      const uint32_t qa = q_issued + (q_last == 0 ? 1u : 0u);
+      if (qa > 0) mbar_wait(bar(L::kQFull), (qa - 1) & 1u);
+      if (q_issued > 0) mbar_wait(bar(L::kQFull + 1), (q_issued - 1) & 1u);
     }
     tc_fence_before();
     __syncthreads();
