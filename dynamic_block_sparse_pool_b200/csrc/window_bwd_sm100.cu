@@ -10,21 +10,21 @@
 //   dkdv  one key tile against the query tiles that see it, for each query
 //         head of its group in turn: every sum has a fixed order, no atomics.
 // Per tile pair the S-type products go to tensor memory as fp32, the
-// element-wise pass writes packed bf16 terms back into the columns it read,
-// and the gradient products take them from there.  dS goes in as two terms,
+// element-wise pass writes packed bf16 terms back into S's columns, and the
+// gradient products take them from there.  For dQ, dS goes in as two terms,
 // hi = bf16(x) and lo = bf16(x - hi): it sums to zero along a row, and where
 // the keys share a common part (they do, in trained attention) dQ is a small
-// difference of large sums that one bf16 term would lose.  P, all of one sign
-// and rounded the same way in the forward, goes in as one (half a step, 2^-9
-// of each weight).
+// difference of large sums that one bf16 term would lose.  dK and dV are sums
+// over queries, whose terms have no such bond: P and dS go in as one term each
+// (half a step, at most 2^-8 of each, as P in the forward).
 //
 // Each tile pair runs as two halves of 64 columns: warps 0-3 own half 0 and
 // warps 4-7 half 1 (one row per thread), each half with its own barriers, so
 // while one half is in its element-wise pass the tensor cores work for the
-// other.  Warp 8 issues the MMAs, warp 9 the TMA loads into a two-stage ring.
-// Tensor memory: S 0-127, dP 128-255, gradients from 256.  Every mbarrier
-// wait is bounded; a timeout sets the device error word and the CTA winds
-// down.
+// other.  Warp 8 issues the MMAs, warp 9 the TMA loads into a ring of two
+// stages (three at D = 64).  Tensor memory: S 0-127, dP 128-255, gradients from
+// 256.  Every mbarrier wait is bounded; a timeout sets the device error word
+// and the CTA winds down.
 #include "bwd_tiles.cuh"
 #include "tile_map.cuh"
 #include "window_attn.cuh"
@@ -40,15 +40,19 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColG = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum : int { kBarFixed = 0, kBarRing = 1, kBarFree = 3, kBarS = 5, kBarP = 7, kBarDrain = 9, kNumBars = 10 };
+// Barriers, with room for three ring stages; kBarR: a half's dP is read out of
+// tensor memory (D = 64), kBarP: its terms are written.
+enum : int { kBarFixed = 0, kBarRing = 1, kBarFree = 4, kBarS = 7, kBarP = 9, kBarR = 11, kBarDrain = 13,
+             kNumBars = 14 };
 
 template <int D>
 struct Smem {
   static constexpr int kTile = BB * D * 2;
-  static constexpr int kFixA = 0, kFixB = kTile;       // the CTA's own two tiles
-  static constexpr int kRingA = 2 * kTile;             // streamed tiles, 2 stages each
-  static constexpr int kRingB = 4 * kTile;
-  static constexpr int kVec = 6 * kTile;               // float [2 stages][-lse2 | -delta][128] (dkdv)
+  static constexpr int kStages = D == 64 ? 3 : 2;       // of the streamed tiles
+  static constexpr int kFixA = 0, kFixB = kTile;        // the CTA's own two tiles
+  static constexpr int kRingA = 2 * kTile;
+  static constexpr int kRingB = kRingA + kStages * kTile;
+  static constexpr int kVec = kRingB + kStages * kTile;  // float [2][-lse2 | -delta][128] (dkdv)
   static constexpr int kBar = kVec + 2 * 2 * BB * 4;
   static constexpr int kSlot = kBar + 8 * kNumBars;
   static constexpr int kBytes = kSlot + 16;
@@ -90,7 +94,8 @@ __device__ __forceinline__ bool cta_begin(Cta& c, uint8_t* smem, unsigned* err) 
   c.abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
   if (c.warp == kMmaWarp) {
     if (c.lane == 0) {
-      for (int i = 0; i < kNumBars; ++i) mbar_init(c.bar(i), (i == kBarP || i == kBarP + 1) ? 4u : 1u);
+      // a half's four warps arrive on kBarP and kBarR
+      for (int i = 0; i < kNumBars; ++i) mbar_init(c.bar(i), i >= kBarP && i < kBarR + 2 ? 4u : 1u);
       *c.abort_flag = 0;
       fence_mbar_init();
     }
@@ -107,19 +112,21 @@ __device__ __forceinline__ bool cta_begin(Cta& c, uint8_t* smem, unsigned* err) 
 
 // After a role gave up, copies and MMAs may still be in flight: they finish
 // (bounded) before shared and tensor memory are released.
+template <int D>
 __device__ __forceinline__ void cta_end(const Cta& c, int n, int issued) {
+  constexpr int ST = Smem<D>::kStages;
   tc_fence_before();
   __syncthreads();
   if (*c.abort_flag) {
     if (c.warp == kMmaWarp && n > 0) {
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_commit(c.bar(kBarDrain));
         mbar_wait(c.bar(kBarDrain), 0u);
       }
       __syncwarp();
     } else if (c.warp == kLoadWarp && c.lane == 0 && n > 0) {
-      for (int b = issued > 2 ? issued - 2 : 0; b < issued; ++b)
-        mbar_wait(c.bar(kBarRing + (b & 1)), (uint32_t)(b >> 1) & 1u);
+      for (int b = issued > ST ? issued - ST : 0; b < issued; ++b)
+        mbar_wait(c.bar(kBarRing + b % ST), (uint32_t)(b / ST) & 1u);
       mbar_wait(c.bar(kBarFixed), 0u);
     }
     tc_fence_before();
@@ -136,6 +143,21 @@ __device__ __forceinline__ void give_up(const Cta& c, unsigned* err) {
   if (c.lane == 0) flag_error(err, kErrTimeout);
 }
 
+// S and dP of a half are in registers (the waits); with `tell`, the MMA issuer
+// learns that dP's columns are free.
+__device__ __forceinline__ void read_out(const Cta& c, int h, uint32_t (&sv)[2][32], uint32_t (&pv)[2][32], bool tell) {
+#pragma unroll
+  for (int cc = 0; cc < 2; ++cc) {
+    tmem_wait_ld_regs(sv[cc]);
+    tmem_wait_ld_regs(pv[cc]);
+  }
+  if (tell) {
+    tc_fence_before();
+    __syncwarp();
+    if (c.lane == 0) mbar_arrive(c.bar(kBarR + h));
+  }
+}
+
 // The loader's part: the fixed tiles of row f0 of head fh, then for it < n
 // the two streamed tiles of head(it), row(it).
 template <int D, typename Where>
@@ -149,10 +171,10 @@ __device__ __forceinline__ int load_tiles(const Cta& c, const CUtensorMap* fa, c
   tma_tile<D>(c.base + L::kFixA, fa, f0, fh, c.bar(kBarFixed));
   tma_tile<D>(c.base + L::kFixB, fb, f0, fh, c.bar(kBarFixed));
   for (int it = 0; it < n; ++it) {
-    const int s = it & 1;
+    const int s = it % L::kStages;
     int head, row;
     where(it, head, row);
-    if (!mbar_wait(c.bar(kBarFree + s), ((uint32_t)(it >> 1) & 1u) ^ 1u) || *c.abort_flag) {
+    if (!mbar_wait(c.bar(kBarFree + s), ((uint32_t)(it / L::kStages) & 1u) ^ 1u) || *c.abort_flag) {
       give_up(c, err);
       break;
     }
@@ -165,42 +187,80 @@ __device__ __forceinline__ int load_tiles(const Cta& c, const CUtensorMap* fa, c
 }
 
 // The MMA issuer's part: S = A a^T and dP = B b^T (A, B fixed, a, b streamed)
-// in halves of 64 streamed rows; then `grads(half, stage offset, first)`.
+// in halves of 64 streamed rows; `grads(half, stage, accumulate)` once a half's
+// terms are written.  The terms lie in S's columns, so the next pair's S
+// follows the gradient products (the MMAs of one thread run in order).  dP's
+// columns are free as soon as they are read: with three ring stages (D = 64)
+// the next pair's dP runs while the half is in its element-wise pass (kEarly);
+// with two its tiles would not have landed.
 template <int D, typename Grads>
 __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, unsigned* err) {
   using L = Smem<D>;
   constexpr uint32_t kTileBytes = L::kTile;
-  const uint64_t dA = smem_desc_sw128(c.base + L::kFixA, 16, 1024), dB = smem_desc_sw128(c.base + L::kFixB, 16, 1024);
-  const uint64_t da = smem_desc_sw128(c.base + L::kRingA, 16, 1024), db = smem_desc_sw128(c.base + L::kRingB, 16, 1024);
-  bool ok = warp_all(mbar_wait(c.bar(kBarFixed), 0u));
-  auto issue_half = [&](int it, int h) {
-    const int s = it & 1;
-    if (h == 0 && !(ok = ok && warp_all(mbar_wait(c.bar(kBarRing + s), (uint32_t)(it >> 1) & 1u)))) return;
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t off = (uint64_t)((s * kTileBytes) >> 4);
-      mma_rows_half<D>(c.tmem + kColS + 64 * h, dA, da + off, h);
-      mma_rows_half<D>(c.tmem + kColP + 64 * h, dB, db + off, h);
-      mma_commit(c.bar(kBarS + h));
-    }
-    __syncwarp();
+  constexpr bool kEarly = L::kStages == 3;
+  const uint32_t base = __shfl_sync(0xffffffffu, c.base, 0), tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
+  const uint64_t dA = smem_desc_sw128(base + L::kFixA, 16, 1024), dB = smem_desc_sw128(base + L::kFixB, 16, 1024);
+  const uint64_t da = smem_desc_sw128(base + L::kRingA, 16, 1024), db = smem_desc_sw128(base + L::kRingB, 16, 1024);
+  int st = 0, st1 = 0;    // ring stages of this pair and of the next
+  uint32_t ring_ph = 0;   // phase of the next pair's stage
+  bool ok = warp_all(mbar_wait(c.bar(kBarFixed), 0u)) && warp_all(mbar_wait(c.bar(kBarRing), 0u));
+  auto scores = [&](int stage, int h) {
+    mma_rows_half<D>(tmem + kColS + 64 * h, dA, da + (uint64_t)(stage * (kTileBytes >> 4)), h);
   };
-  issue_half(0, 0);
-  if (ok) issue_half(0, 1);
-  for (int it = 0; it < n && ok; ++it) {
-    const int s = it & 1;
-    for (int h = 0; h < 2 && ok; ++h) {
-      if (!(ok = warp_all(mbar_wait(c.bar(kBarP + h), (uint32_t)it & 1u)))) break;
-      tc_fence_after();
+  auto dprobs = [&](int stage, int h) {
+    mma_rows_half<D>(tmem + kColP + 64 * h, dB, db + (uint64_t)(stage * (kTileBytes >> 4)), h);
+  };
+  if (ok) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       if (elect_one()) {
-        grads(h, (uint64_t)((s * kTileBytes) >> 4), it > 0 || h > 0);
-        if (h == 1) mma_commit(c.bar(kBarFree + s));
+        scores(0, h);
+        dprobs(0, h);
+        mma_commit(c.bar(kBarS + h));
       }
       __syncwarp();
-      // half h of the next pair overwrites half h's packed terms only after
-      // the gradient products have read them (MMAs of one thread run in order)
-      if (it + 1 < n) issue_half(it + 1, h);
     }
+  }
+  for (int it = 0; it < n && ok; ++it) {
+    const bool more = it + 1 < n;
+    const uint32_t ph = (uint32_t)it & 1u;
+    st1 = st + 1;
+    if (st1 == L::kStages) {
+      st1 = 0;
+      ring_ph ^= 1u;
+    }
+    if (kEarly && more) {
+      if (!(ok = warp_all(mbar_wait(c.bar(kBarRing + st1), ring_ph)))) break;
+      if (!(ok = warp_all(mbar_wait(c.bar(kBarR), ph)) && warp_all(mbar_wait(c.bar(kBarR + 1), ph)))) break;
+      tc_fence_after();
+      if (elect_one()) {  // both halves at once: half as many MMAs
+        const uint64_t b0 = db + (uint64_t)(st1 * (kTileBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + kColP, dB + kstep<D>(kk), b0 + kstep<D>(kk), idesc_bf16_f32(BB, BB, false), kk > 0 ? 1u : 0u);
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!(ok = ok && warp_all(mbar_wait(c.bar(kBarP + h), ph)))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        grads(h, (uint64_t)(st * (kTileBytes >> 4)), it > 0 || h > 0);
+        if (h == 1) mma_commit(c.bar(kBarFree + st));
+      }
+      __syncwarp();
+      if (more) {
+        if (!kEarly && h == 0 && !(ok = warp_all(mbar_wait(c.bar(kBarRing + st1), ring_ph)))) break;
+        if (elect_one()) {
+          scores(st1, h);
+          if (!kEarly) dprobs(st1, h);
+          mma_commit(c.bar(kBarS + h));
+        }
+        __syncwarp();
+      }
+    }
+    st = st1;
   }
   if (!ok) give_up(c, err);
 }
@@ -228,9 +288,10 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }, err);
   } else if (c.warp == kMmaWarp) {
     if (n > 0) {
-      const uint64_t dKm = smem_desc_sw128(c.base + L::kRingA, kSubBytes, 1024);
+      const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
+      const uint64_t dKm = smem_desc_sw128(__shfl_sync(0xffffffffu, c.base, 0) + L::kRingA, kSubBytes, 1024);
       issue_mmas<D>(c, n, [&](int h, uint64_t off, bool accumulate) {
-        mma_grad_half<D>(c.tmem + kColG, c.tmem + kColS, dKm + off, h, accumulate);  // dQ += dS K
+        mma_grad_half<D>(tmem + kColG, tmem + kColS, dKm + off, h, accumulate);  // dQ += dS K
       }, err);
     }
   } else {
@@ -250,32 +311,34 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool whole = all_visible(p.w, q0, q1, k0, k0 + BB);
       if (!(ok = warp_all(mbar_wait(c.bar(kBarS + h), (uint32_t)it & 1u)))) break;
       tc_fence_after();
+      uint32_t sv[2][32], pv[2][32];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        tmem_ld32(c.tmem + lanes + kColS + 64 * h + 32 * cc, sv[cc]);
+        tmem_ld32(c.tmem + lanes + kColP + 64 * h + 32 * cc, pv[cc]);
+      }
+      read_out(c, h, sv, pv, D == 64);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const uint32_t col = 64u * h + 32u * cc;
-        uint32_t sv[32], pv[32];
-        tmem_ld32(c.tmem + lanes + kColS + col, sv);
-        tmem_ld32(c.tmem + lanes + kColP + col, pv);
-        tmem_wait_ld_regs(sv);
-        tmem_wait_ld_regs(pv);
         if (!whole) {
           const int k = k0 + (int)col;
           const uint32_t m = below(hi - k) & (~below(lo - k) | below(p.w.sink - k));
 #pragma unroll
           for (int u = 0; u < 32; ++u)
             if (!((m >> u) & 1u)) {
-              sv[u] = 0xff800000u;  // -inf: P = 0
-              pv[u] = 0u;
+              sv[cc][u] = 0xff800000u;  // -inf: P = 0
+              pv[cc][u] = 0u;
             }
         }
         uint32_t dh[16], dl[16];
 #pragma unroll
         for (int m = 0; m < 16; ++m) {
           float t0, t1, g0, g1;
-          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sv[2 * m]), __uint_as_float(sv[2 * m + 1])), sc2, nl2),
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sv[cc][2 * m]), __uint_as_float(sv[cc][2 * m + 1])), sc2, nl2),
                        t0, t1);
           const uint64_t p2 = pack_f32x2(exp2_approx(t0), exp2_approx(t1));
-          const uint64_t d2 = add_f32x2(pack_f32x2(__uint_as_float(pv[2 * m]), __uint_as_float(pv[2 * m + 1])), nd2);
+          const uint64_t d2 = add_f32x2(pack_f32x2(__uint_as_float(pv[cc][2 * m]), __uint_as_float(pv[cc][2 * m + 1])), nd2);
           unpack_f32x2(mul_f32x2(p2, d2), g0, g1);
           split_pair(g0, g1, dh[m], dl[m]);
         }
@@ -287,7 +350,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       __syncwarp();
       if (c.lane == 0) mbar_arrive(c.bar(kBarP + h));
     }
-    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFree + ((n - 1) & 1)), (uint32_t)((n - 1) >> 1) & 1u));
+    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFree + (n - 1) % L::kStages), (uint32_t)((n - 1) / L::kStages) & 1u));
     if (!ok) {
       give_up(c, err);
     } else {
@@ -308,7 +371,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     }
   }
-  cta_end(c, n, issued);
+  cta_end<D>(c, n, issued);
 }
 
 template <int D>
@@ -337,11 +400,12 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }, err);
   } else if (c.warp == kMmaWarp) {
     if (n > 0) {
-      const uint64_t dQm = smem_desc_sw128(c.base + L::kRingA, kSubBytes, 1024);
-      const uint64_t dOm = smem_desc_sw128(c.base + L::kRingB, kSubBytes, 1024);
+      const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0), base = __shfl_sync(0xffffffffu, c.base, 0);
+      const uint64_t dQm = smem_desc_sw128(base + L::kRingA, kSubBytes, 1024);
+      const uint64_t dOm = smem_desc_sw128(base + L::kRingB, kSubBytes, 1024);
       issue_mmas<D>(c, n, [&](int h, uint64_t off, bool accumulate) {
-        mma_grad_half<D, false>(c.tmem + kColV, c.tmem + kColS, dOm + off, h, accumulate);  // dV += P^T dO
-        mma_grad_half<D>(c.tmem + kColK, c.tmem + kColP, dQm + off, h, accumulate);         // dK += dS^T Q
+        mma_grad_half<D, false>(tmem + kColV, tmem + kColS, dOm + off, h, accumulate);       // dV += P^T dO
+        mma_grad_half<D, false>(tmem + kColK, tmem + kColS + 16, dQm + off, h, accumulate);  // dK += dS^T Q
       }, err);
     }
   } else {
@@ -378,14 +442,16 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         break;
       }
       tc_fence_after();
+      uint32_t sv[2][32], pv[2][32];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        tmem_ld32(c.tmem + lanes + kColS + 64 * h + 32 * cc, sv[cc]);
+        tmem_ld32(c.tmem + lanes + kColP + 64 * h + 32 * cc, pv[cc]);
+      }
+      read_out(c, h, sv, pv, D == 64);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const uint32_t col = 64u * h + 32u * cc;
-        uint32_t sv[32], pv[32];
-        tmem_ld32(c.tmem + lanes + kColS + col, sv);
-        tmem_ld32(c.tmem + lanes + kColP + col, pv);
-        tmem_wait_ld_regs(sv);
-        tmem_wait_ld_regs(pv);
         if (!whole) {
           // query i of the tile sees key u iff t >= u - right and (u < sink or t <= u + left)
           const int t0 = p.w.off + q0 + (int)col;
@@ -393,34 +459,33 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((m >> e) & 1u)) {
-              sv[e] = 0xff800000u;
-              pv[e] = 0u;
+              sv[cc][e] = 0xff800000u;
+              pv[cc][e] = 0u;
             }
         }
-        uint32_t ph[16], dh[16], dl[16];
+        uint32_t ph[16], dh[16];
 #pragma unroll
         for (int m = 0; m < 16; ++m) {
           const int qq = (int)col + 2 * m;  // even: the pairs are 8-byte aligned
           float t0, t1, g0, g1;
-          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sv[2 * m]), __uint_as_float(sv[2 * m + 1])), sc2,
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sv[cc][2 * m]), __uint_as_float(sv[cc][2 * m + 1])), sc2,
                                  *reinterpret_cast<const uint64_t*>(nl + qq)), t0, t1);
           const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
           ph[m] = pack_bf16(p0, p1);
-          const uint64_t d2 = add_f32x2(pack_f32x2(__uint_as_float(pv[2 * m]), __uint_as_float(pv[2 * m + 1])),
+          const uint64_t d2 = add_f32x2(pack_f32x2(__uint_as_float(pv[cc][2 * m]), __uint_as_float(pv[cc][2 * m + 1])),
                                         *reinterpret_cast<const uint64_t*>(nd + qq));
           unpack_f32x2(mul_f32x2(pack_f32x2(p0, p1), d2), g0, g1);
-          split_pair(g0, g1, dh[m], dl[m]);
+          dh[m] = pack_bf16(g0, g1);
         }
         tmem_st16(c.tmem + lanes + kColS + col, ph);
-        tmem_st16(c.tmem + lanes + kColP + col, dh);
-        tmem_st16(c.tmem + lanes + kColP + col + 16, dl);
+        tmem_st16(c.tmem + lanes + kColS + col + 16, dh);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (c.lane == 0) mbar_arrive(c.bar(kBarP + h));
     }
-    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFree + ((n - 1) & 1)), (uint32_t)((n - 1) >> 1) & 1u));
+    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFree + (n - 1) % L::kStages), (uint32_t)((n - 1) / L::kStages) & 1u));
     if (!ok) {
       give_up(c, err);
     } else {
@@ -441,7 +506,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
     }
   }
-  cta_end(c, n, issued);
+  cta_end<D>(c, n, issued);
 }
 
 template <int D>

@@ -12,8 +12,9 @@ eP = 2 eS + 2^-19 relative (the exponentials and the row's reference add a few
     lse:  eP + 2^-22 |lse|.
 Gradients, given o and lse as inputs: eW = eP + 2^-22 |lse| for P; the fp32
 sums of D terms put eD = 2 D E (sum |do v| + sum |do o|) on dP - delta; so
-dS is off by fS = p (eW |dP - delta| + eD) + t |dS| with t = 2^-16 (bf16: two
-terms) or 2 E:
+dS is off by fS = p (eW |dP - delta| + eD) + t |dS| with t = 2 E in fp32; in
+bf16 it enters dq as two terms, hi + lo = dS (1 + 2^-8 2^-8): t = 2^-16, and dk
+as one term, rounded once: t = uP = 2^-8 (half a step, as P for dv):
     dq:   u |dq| + scale (sum fS |k| + n E sum |dS k|),  dk alike with |q|;
     dv:   u |dv| + (eW + uP + n E) sum p |do|."""
 import math
@@ -108,15 +109,16 @@ def check_backward(q, k, v, do, off, left, right, sink, scale=None):
     ds = p * (dp - delta)
     ew = ep + 2.0 ** -22 * lse.abs().clamp(max=1e30)
     ed = 2 * D * E * (dd.abs() @ vd.abs().transpose(2, 3) + (dd * od).abs().sum(-1, keepdim=True))
-    t = 2.0 ** -16 if dt == torch.bfloat16 else 2 * E
-    fs = p * (ew * (dp - delta).abs() + ed) + t * ds.abs()
+    fs = p * (ew * (dp - delta).abs() + ed)
+    fsq = fs + (2.0 ** -16 if dt == torch.bfloat16 else 2 * E) * ds.abs()
+    fsk = fs + (UP[dt] + 2 * E) * ds.abs()
     grp = lambda x: x.view(B, Hk, H // Hk, *x.shape[2:]).sum(2)  # noqa: E731
     n = ok.sum(-1).max().item()
     m = ok.sum(0).max().item() * (H // Hk)
     dq = sc * ds @ kd
-    inside(got[0], dq, U[dt] * dq.abs() + sc * (fs + n * E * ds.abs()) @ kd.abs(), "dq")
+    inside(got[0], dq, U[dt] * dq.abs() + sc * (fsq + n * E * ds.abs()) @ kd.abs(), "dq")
     dk = grp(sc * ds.transpose(2, 3) @ qd)
-    inside(got[1], dk, U[dt] * dk.abs() + grp(sc * (fs + m * E * ds.abs()).transpose(2, 3) @ qd.abs()), "dk")
+    inside(got[1], dk, U[dt] * dk.abs() + grp(sc * (fsk + m * E * ds.abs()).transpose(2, 3) @ qd.abs()), "dk")
     dv = grp(p.transpose(2, 3) @ dd)
     inside(got[2], dv, U[dt] * dv.abs() + grp(((ew + UP[dt] + m * E) * p).transpose(2, 3) @ dd.abs()), "dv")
     return got
