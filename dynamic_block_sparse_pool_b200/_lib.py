@@ -52,7 +52,8 @@ SIGNATURES = {
                                  _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dsa_window_attn_bwd_workspace_size": (_sz, [_i, _i, _i]),
     "dsa_window_attn_decode": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _i,
-                                    _vp, _vp, _vp]),
+                                    _vp, _vp, _vp, _sz, _vp]),
+    "dsa_window_attn_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "dsa_pack8": (_i, [_vp, _i, _sz, _i, _vp, _vp, _vp]),
     "dsa_unpack8": (_i, [_vp, _vp, _i, _sz, _i, _vp, _vp]),
     "dsa_select_topp_static": (_i, [_vp, _i, _i, _f, _vp, _vp, _vp, _vp, _vp]),

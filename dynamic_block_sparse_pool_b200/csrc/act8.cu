@@ -31,9 +31,10 @@ pack8_kernel(const T* __restrict__ x, long long rows, int8_t* __restrict__ codes
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float v[8], scale;
-    values8(raw[u], v);
-    const uint2 c = encode8<TPR>(v, scale);
+    Pair v[4];
+    float scale;
+    values(raw[u], v);
+    const uint2 c = encode8<TPR>(v, top_bits(raw[u]), scale);
     const long long r = r0 + u * RPC;
     if (r < rows) {
       *reinterpret_cast<uint2*>(codes + r * D + 8 * sub) = c;
@@ -58,10 +59,12 @@ unpack8_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scale
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float v[8];
-    values8(raw[u], v);
+    Pair v[4];
+    values(raw[u], v);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) v[m] = mul_f32x2(v[m], both(raw[u].scale));
     const long long r = r0 + u * RPC;
-    if (r < rows) store8(x + r * D + 8 * sub, v);
+    if (r < rows) store(x + r * D + 8 * sub, v);
   }
 }
 

@@ -65,7 +65,7 @@ dsa_status check_norm_rope(const void* xq, const void* xk, const float* xq_scale
   if ((xq_scale == nullptr) != (xk_scale == nullptr))
     return fail(DSA_ERR_INVALID_ARG, "xq_scale and xk_scale must both be set or both be NULL");
   if (B < 1 || N < 1) return fail(DSA_ERR_INVALID_ARG, "B and N must be >= 1 (got %d, %d)", B, N);
-  if ((long long)B * N > INT_MAX) return fail(DSA_ERR_INVALID_ARG, "B*N exceeds 2^31 - 1");
+  if ((long long)B * N > INT_MAX - 65536) return fail(DSA_ERR_INVALID_ARG, "B*N exceeds 2^31 - 65537");
   if (Hq < 1 || Hk < 1 || Hq > 65535 || Hk > 65535)
     return fail(DSA_ERR_INVALID_ARG, "Hq and Hk must be 1..65535 (got %d, %d)", Hq, Hk);
   if (D != 64 && D != 128) return fail(DSA_ERR_INVALID_ARG, "head_dim D must be 64 or 128 (got %d)", D);
@@ -195,26 +195,55 @@ dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, cons
   return launched(e, "window_attn_bwd launch");
 }
 
-dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
-                                  const int64_t* kv_strides, dsa_dtype dt, int B, int H, int Hk,
-                                  int Nq, int cap, int D, float scale, const int32_t* lens,
-                                  int left, int sink, void* out, float* lse, void* stream) {
-  dsa::api_set_last_error("");
-  if (!q || !k || !v || !kv_strides || !lens || !out)
-    return fail(DSA_ERR_INVALID_ARG, "null q, k, v, kv_strides, lens or out");
+static dsa_status check_decode(dsa_dtype dt, int B, int H, int Hk, int Nq, int cap, int D, float scale, int sink) {
   dsa_status st = check_heads(B, H, Hk, D, scale, sink, dt);
   if (st != DSA_OK) return st;
   if (Nq < 1 || Nq > 128) return fail(DSA_ERR_INVALID_ARG, "Nq must be 1..128 (got %d)", Nq);
   if (cap < 1 || cap > (1 << 27)) return fail(DSA_ERR_INVALID_ARG, "cap must be 1..2^27 (got %d)", cap);
+  return DSA_OK;
+}
+
+static size_t decode_ws_bytes(const dsa::DecodePlan& p, int B, int H, int Nq, int D) {
+  return p.groups == 1 ? 0 : (size_t)p.groups * B * H * Nq * (D + 2) * sizeof(float);
+}
+
+size_t dsa_window_attn_decode_workspace_size(dsa_dtype dt, int B, int H, int Hk, int Nq, int cap, int D, int left,
+                                             int sink) {
+  dsa::api_set_last_error("");
+  if (check_decode(dt, B, H, Hk, Nq, cap, D, 1.f, sink) != DSA_OK) return 0;
+  return decode_ws_bytes(dsa::decode_plan(dt == DSA_BF16, B, H, Hk, Nq, cap, D, bound(left), std::min(sink, cap)), B,
+                         H, Nq, D);
+}
+
+dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
+                                  const int64_t* kv_strides, dsa_dtype dt, int B, int H, int Hk,
+                                  int Nq, int cap, int D, float scale, const int32_t* lens,
+                                  int left, int sink, void* out, float* lse, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  dsa::api_set_last_error("");
+  if (!q || !k || !v || !kv_strides || !lens || !out)
+    return fail(DSA_ERR_INVALID_ARG, "null q, k, v, kv_strides, lens or out");
+  dsa_status st = check_decode(dt, B, H, Hk, Nq, cap, D, scale, sink);
+  if (st != DSA_OK) return st;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lens, 4) ||
-      !aligned(lse, 4))
-    return fail(DSA_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned, lens and lse 4-byte aligned");
+      !aligned(lse, 4) || !aligned(workspace, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q, k, v, out and workspace must be 16-byte aligned, lens and lse 4-byte aligned");
   if ((st = check_strides(kv_strides, dt == DSA_BF16 ? 8 : 4, "kv_strides")) != DSA_OK) return st;
+  const int dims[3] = {B, Hk, cap};
+  for (int i = 0; i < 6; ++i)
+    if (dims[i % 3] > 1 && (kv_strides[i] < D || kv_strides[i] >= (1ll << 38)))
+      return fail(DSA_ERR_INVALID_ARG, "kv_strides[%d] = %lld: rows must not overlap", i, (long long)kv_strides[i]);
   dsa::DecodeAttn a = {};
   a.B = B; a.H = H; a.Hk = Hk; a.group = H / Hk; a.Nq = Nq; a.cap = cap;
   a.scale = scale;
   a.left = bound(left);
   a.sink = std::min(sink, cap);
+  const dsa::DecodePlan plan = dsa::decode_plan(dt == DSA_BF16, B, H, Hk, Nq, cap, D, a.left, a.sink);
+  const size_t need = decode_ws_bytes(plan, B, H, Nq, D);
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return fail(DSA_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu needed", workspace ? ws_bytes : 0, need);
+  a.groups = plan.groups;
+  a.ws = static_cast<float*>(workspace);
   a.q = q; a.k = k; a.v = v;
   for (int i = 0; i < 3; ++i) {
     a.ks[i] = kv_strides[i];
@@ -223,9 +252,12 @@ dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
   a.lens = lens;
   a.out = out;
   a.lse = lse;
-  if ((st = dsa::api_checked_device(&a.err)) != DSA_OK || (st = sm_count(&a.num_sms)) != DSA_OK) return st;
-  return launched(dsa::launch_window_decode(a, dt == DSA_BF16, D, static_cast<cudaStream_t>(stream)),
-                  "window_attn_decode launch");
+  if ((st = dsa::api_checked_device(&a.err)) != DSA_OK) return st;
+  const char* why = nullptr;
+  const cudaError_t e =
+      dsa::launch_window_decode(a, plan, dt == DSA_BF16, D, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why) return fail(DSA_ERR_CUDA, "window_attn_decode: %s", why);
+  return launched(e, "window_attn_decode launch");
 }
 
 dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table) {
@@ -279,7 +311,7 @@ dsa_status dsa_qk_norm_rope(const void* xq, const void* xk, const float* xq_scal
 }
 
 size_t dsa_qk_norm_rope_bwd_workspace_size(int D) {
-  return D == 64 || D == 128 ? (size_t)dsa::kNormRopeBwdCtas * 2 * D * sizeof(float) : 0;
+  return D == 64 || D == 128 ? (size_t)dsa::kNormRopeBwdCtas * D * sizeof(float) : 0;
 }
 
 dsa_status dsa_qk_norm_rope_bwd(const void* dq, const void* dk, const void* xq, const void* xk,

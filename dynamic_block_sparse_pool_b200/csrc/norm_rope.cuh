@@ -6,9 +6,9 @@
 
 namespace dsa {
 
-// Most CTAs the backward uses (four on each of 148 SMs); each leaves its
-// share of the two weight gradients in the workspace.
-constexpr int kNormRopeBwdCtas = 592;
+// Most CTAs the backward uses (three on each of 148 SMs); each leaves its
+// share of one weight gradient in the workspace.
+constexpr int kNormRopeBwdCtas = 444;
 
 struct RopeArgs {
   const float2* table;      // per axis a: [len[a]][pairs[a]] (cos, sin), axes one after another
@@ -47,7 +47,7 @@ struct NormRopeBwd {
   void *dxq, *dxk;
   long long dqb, dqn, dqh, dkb, dkn, dkh;
   float *dwq, *dwk;                  // NULL: not wanted
-  float* part;                       // kNormRopeBwdCtas * 2 * D floats
+  float* part;                       // kNormRopeBwdCtas * D floats
   unsigned* err;
 };
 

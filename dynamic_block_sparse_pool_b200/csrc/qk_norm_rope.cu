@@ -34,17 +34,17 @@ using namespace rows8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Cosine and sine of the pairs a thread's eight values belong to: four
-// neighbouring pairs, or (halves) eight, the partner values being in the
-// thread D / 16 further on.
+// The turn of a thread's eight values, as y = x c + partner(x) s with the
+// signs in s.  Neighbouring pairs: the partner is the other value of the pair.
+// Halves: it is the same value of the thread D / 16 further on.
 template <int D, bool HALVES>
 struct Turn {
-  static constexpr int kPairs = HALVES ? 8 : 4;
-  float c[kPairs], s[kPairs];
+  Pair c[4], s[4];
 
   // The token's angles from the tables.  A position below 0 does not turn;
   // one past its axis' table is reported and does not turn either.
   __device__ __forceinline__ void load(const RopeArgs& a, int b, int n, int sub, unsigned* err) {
+    constexpr int kPairs = HALVES ? 8 : 4;
     const int32_t* p = a.pos + b * a.pos_bstride + (long long)n * 3;
     const int first = HALVES ? (8 * sub) % (D / 2) : 4 * sub;
     int at[3];
@@ -56,6 +56,7 @@ struct Turn {
       at[x] = v >= a.len[x] ? -1 : v;
     }
     if (bad && sub == 0) flag_error(err, kErrPosition);
+    float2 t[kPairs];
 #pragma unroll
     for (int m = 0; m < kPairs; ++m) {
       int i = first + m, base = 0, x = 0;
@@ -71,32 +72,41 @@ struct Turn {
       }
       const int pa = x == 0 ? a.pairs[0] : x == 1 ? a.pairs[1] : a.pairs[2];
       const int v = x == 0 ? at[0] : x == 1 ? at[1] : at[2];
-      float2 t = make_float2(1.f, 0.f);
-      if (v >= 0 && i < pa) t = __ldg(a.table + base + (long long)v * pa + i);
-      c[m] = t.x;
-      s[m] = t.y;
+      t[m] = make_float2(1.f, 0.f);
+      if (v >= 0 && i < pa) t[m] = __ldg(a.table + base + (long long)v * pa + i);
     }
-  }
-
-  // Turns the thread's eight values (back: by the opposite angle).
-  template <bool BACK>
-  __device__ __forceinline__ void apply(float (&v)[8], int sub) const {
     if (HALVES) {
-      // first half: a cos - b sin; second half: b cos + a sin
-      const bool lower = sub < D / 16;
-      const float sign = (lower != BACK) ? -1.f : 1.f;
+      const float sign = sub < D / 16 ? -1.f : 1.f;  // first half: a cos - b sin
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_xor_sync(0xffffffffu, v[e], D / 16);
-        v[e] = fmaf(v[e], c[e % kPairs], sign * o * s[e % kPairs]);
+      for (int m = 0; m < 4; ++m) {
+        c[m] = pair(t[(2 * m) % kPairs].x, t[(2 * m + 1) % kPairs].x);
+        s[m] = pair(sign * t[(2 * m) % kPairs].y, sign * t[(2 * m + 1) % kPairs].y);
       }
     } else {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float a = v[2 * m], b = v[2 * m + 1], t = BACK ? -s[m % kPairs] : s[m % kPairs];
-        v[2 * m] = fmaf(a, c[m % kPairs], -b * t);
-        v[2 * m + 1] = fmaf(a, t, b * c[m % kPairs]);
+        c[m] = both(t[m].x);
+        s[m] = pair(-t[m].y, t[m].y);
       }
+    }
+  }
+  // The opposite turn.
+  __device__ __forceinline__ void reverse() {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) s[m] = mul_f32x2(s[m], both(-1.f));
+  }
+  __device__ __forceinline__ void apply(Pair (&v)[4]) const {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      Pair o;
+      if (HALVES) {
+        float x, y;
+        unpack_f32x2(v[m], x, y);
+        o = pair(__shfl_xor_sync(0xffffffffu, x, D / 16), __shfl_xor_sync(0xffffffffu, y, D / 16));
+      } else {
+        o = swapped(v[m]);
+      }
+      v[m] = fma_f32x2(v[m], c[m], mul_f32x2(o, s[m]));
     }
   }
 };
@@ -111,24 +121,19 @@ struct Side {
   const float* w;
 };
 
-__device__ __forceinline__ void load_weight(const float* w, int sub, float (&v)[8]) {
-  if (w == nullptr) {
+__device__ __forceinline__ void load_weight(const float* w, int sub, Pair (&v)[4]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 1.f;
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = __ldg(w + 8 * sub + e);
+  for (int m = 0; m < 4; ++m)
+    v[m] = w ? pair(__ldg(w + 8 * sub + 2 * m), __ldg(w + 8 * sub + 2 * m + 1)) : both(1.f);
 }
 
 template <typename TIn>
-__device__ __forceinline__ void fetch(const Side<TIn>& s, int b, int n, int h, int N, int sub, Raw<TIn>& r) {
-  load8(s.x + b * s.b + n * s.n + h * s.h + 8 * sub, r);
+__device__ __forceinline__ void fetch(const TIn* p, const float*, long long, Raw<TIn>& r) {
+  load8(p, r);
 }
-__device__ __forceinline__ void fetch(const Side<int8_t>& s, int b, int n, int h, int N, int sub,
-                                      Raw<int8_t>& r) {
-  load8(s.x + b * s.b + n * s.n + h * s.h + 8 * sub, r);
-  r.scale = __ldg(s.xs + ((long long)b * N + n) * s.heads + h);
+__device__ __forceinline__ void fetch(const int8_t* p, const float* scales, long long row, Raw<int8_t>& r) {
+  load8(p, r);
+  r.scale = __ldg(scales + row);
 }
 
 template <typename TIn, typename TOut>
@@ -147,166 +152,259 @@ struct FwdArgs {
 // Grid: x = tokens / 8 (one warp per token), y = parts of the token's heads.
 // A step is kUnroll * (32 / TPR) heads of q or of k.
 template <typename TIn, typename TOut, int D, bool HALVES, bool SAVE8, int UNROLL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(TIn) == 4 ? 3 : 4)
 qk_norm_rope_kernel(const FwdArgs<TIn, TOut> a) {
   constexpr int TPR = D / 8, RPW = 32 / TPR, kStep = UNROLL * RPW;
   const int lane = threadIdx.x & 31, sub = lane % TPR, slot = lane / TPR;
-  const long long token = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (token >= a.tokens) return;
-  const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
+  const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (token >= (int)a.tokens) return;
+  const int b = token / a.N, n = token - b * a.N;
+  const long long ystep = (long long)a.N * D;  // from head to head in y
   const int steps_q = ceil_div(a.q.heads, kStep), steps = steps_q + ceil_div(a.k.heads, kStep);
   const int per = ceil_div(steps, (int)gridDim.y);
   const int s0 = blockIdx.y * per, s1 = min(steps, s0 + per);
   Turn<D, HALVES> turn;
-  float w[8];
+  Pair w[4];
+  const TIn* px = nullptr;    // running pointers over the side's heads
+  TOut* py = nullptr;
   for (int st = s0; st < s1; ++st) {
     const bool is_k = st >= steps_q;
     const Side<TIn>& side = is_k ? a.k : a.q;
     const int heads = side.heads, h0 = (is_k ? st - steps_q : st) * kStep + slot;
+    if (st == s0 || st == steps_q) {
+      px = side.x + b * side.b + n * side.n + h0 * side.h + 8 * sub;
+      py = (is_k ? a.yk : a.yq) + ((long long)b * heads + h0) * ystep + (long long)n * D + 8 * sub;
+    }
     Raw<TIn> raw[UNROLL];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      fetch(side, b, n, min(h0 + u * RPW, heads - 1), a.N, sub, raw[u]);
+    for (int u = 0; u < UNROLL; ++u) {
+      // (a lane past the heads reads its first row again)
+      const int h = h0 + u * RPW < heads ? u * RPW : 0;
+      fetch(px + (h0 < heads ? h : 0) * side.h - (h0 < heads ? 0 : (h0 - heads + 1) * side.h), side.xs,
+            (long long)token * heads + min(h0 + h, heads - 1), raw[u]);
+    }
     if (st == s0) turn.load(a.rope, b, n, sub, a.err);
     if (st == s0 || st == steps_q) load_weight(side.w, sub, w);
-    TOut* y = is_k ? a.yk : a.yq;
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int h = h0 + u * RPW;
-      float v[8];
-      values8(raw[u], v);
-      if (SAVE8) {
+      Pair v[4];
+      values(raw[u], v);
+      if constexpr (SAVE8) {
         float scale;
-        const uint2 c = encode8<TPR>(v, scale);
+        const uint2 c = encode8<TPR>(v, top_bits(raw[u]), scale);
         if (h < heads) {
-          const long long row = token * heads + h;
+          const long long row = (long long)token * heads + h;
           *reinterpret_cast<uint2*>((is_k ? a.ck : a.cq) + row * D + 8 * sub) = c;
           if (sub == 0) (is_k ? a.sk : a.sq)[row] = scale;
         }
       }
-      float ss = 0.f;
+      Pair ss = 0ull;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-      const float r = rsqrtf(row_sum<TPR>(ss) * (1.0f / D) + a.eps);
+      for (int m = 0; m < 4; ++m) ss = fma_f32x2(v[m], v[m], ss);
+      // (8-bit rows: v holds the codes, the row is scale * v)
+      const float scale = scale_of(raw[u]);
+      const Pair r = both(scale * rsqrtf(scale * scale * row_sum<TPR>(added(ss)) * (1.0f / D) + a.eps));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
-      turn.template apply<false>(v, sub);
-      if (h < heads) store8(y + (((long long)b * heads + h) * a.N + n) * D + 8 * sub, v);
+      for (int m = 0; m < 4; ++m) v[m] = mul_f32x2(mul_f32x2(v[m], r), w[m]);
+      turn.apply(v);
+      if (h < heads) store(py + u * RPW * ystep, v);
     }
+    px += kStep * side.h;
+    py += kStep * ystep;
   }
 }
 
+// One side of the backward.
+template <typename TX, typename TG>
+struct BwdSide {
+  Side<TX> x;
+  const TG* g;         // gradient of y, [B, heads, N, D]
+  TG* d;               // gradient of x
+  long long b, n, h;   // its strides, in elements
+};
+
 template <typename TX, typename TG>
 struct BwdArgs {
-  Side<TX> q, k;
-  const TG *gq, *gk;        // gradients of y, [B, heads, N, D]
-  TG *dq, *dk;              // gradients of x
-  long long dqb, dqn, dqh, dkb, dkn, dkh;  // their strides, in elements
-  float* part;              // [CTAs][2][D]: the CTA's share of dwq | dwk
+  BwdSide<TX, TG> q, k;
+  int parts_q;         // parts of q's heads; the other parts are k's
+  int heads_per_part;
+  float* part;         // [parts][gridDim.x][D]: the CTAs' shares of dwq, then of dwk
   int N;
-  long long tokens;
+  long long tokens;    // < 2^31 - 2^16, so a place past the last one fits too
   float eps;
   RopeArgs rope;
   unsigned* err;
 };
 
-// Persistent: warp g of all the warps takes tokens g, g + warps, ... (the grid
-// does not depend on the data, so each thread sums dw over the same rows in
-// the same order every time), then the CTA's threads are added in order.
-template <typename TX, typename TG, int D, bool HALVES, int UNROLL>
-__global__ void __launch_bounds__(kThreads)
+// A thread's eight values into its slots, and back.
+__device__ __forceinline__ void fetch_async(uint32_t slot, const __nv_bfloat16* p, const float*) { copy_async<16>(slot, p); }
+__device__ __forceinline__ void fetch_async(uint32_t slot, const float* p, const float*) {
+  copy_async<16>(slot, p);
+  copy_async<16>(slot + 16 * kThreads, p + 4);
+}
+__device__ __forceinline__ void fetch_async(uint32_t slot, const int8_t* p, const float* scale) {
+  copy_async<8>(slot, p);
+  copy_async<4>(slot + 8, scale);
+}
+__device__ __forceinline__ void read_slot(const uint4* slot, Raw<__nv_bfloat16>& r) { r.v = slot[0]; }
+__device__ __forceinline__ void read_slot(const uint4* slot, Raw<float>& r) {
+  r.v = slot[0];
+  r.w = slot[kThreads];
+}
+__device__ __forceinline__ void read_slot(const uint4* slot, Raw<int8_t>& r) {
+  r.v = make_uint2(slot->x, slot->y);
+  r.scale = __uint_as_float(slot->z);
+}
+
+// Steps of the backward whose loads are in flight: enough bytes for HBM's
+// latency with three CTAs on an SM (32 or 64 KB of shared memory each).
+constexpr uint32_t kDepth = 4;
+template <typename TX, typename TG>
+constexpr int bwd_slots() { return Slots<TX>::kCount + Slots<TG>::kCount; }
+
+// Grid: x = CTAs over the tokens, y = parts of q's, then of k's heads.  Warp g
+// of a part takes tokens g, g + warps, ... (the grid does not depend on the
+// data, so each thread sums dw over the same rows in the same order every
+// time), then the CTA's threads are added in order.  A step is one row per
+// thread; its loads go out kDepth - 1 steps ahead.
+template <typename TX, typename TG, int D, bool HALVES>
+__global__ void __launch_bounds__(kThreads, 3)
 qk_norm_rope_bwd_kernel(const BwdArgs<TX, TG> a) {
-  constexpr int TPR = D / 8, RPW = 32 / TPR, kStep = UNROLL * RPW;
+  constexpr int TPR = D / 8, RPW = 32 / TPR, SX = Slots<TX>::kCount, SLOTS = bwd_slots<TX, TG>();
+  extern __shared__ __align__(16) uint4 ring[];  // [kDepth][SLOTS][kThreads]
   __shared__ float red[kWarps * RPW][D];
   const int lane = threadIdx.x & 31, sub = lane % TPR, slot = lane / TPR, warp = threadIdx.x >> 5;
-  const int steps_q = ceil_div(a.q.heads, kStep), steps = steps_q + ceil_div(a.k.heads, kStep);
-  const int per = ceil_div(steps, (int)gridDim.y);
-  const int s0 = blockIdx.y * per, s1 = min(steps, s0 + per);
-  float dwq[8], dwk[8];
+  const bool is_k = blockIdx.y >= a.parts_q;
+  const BwdSide<TX, TG>& side = is_k ? a.k : a.q;
+  const int heads = side.x.heads;
+  const int ha = (is_k ? blockIdx.y - a.parts_q : blockIdx.y) * a.heads_per_part, hz = min(heads, ha + a.heads_per_part);
+  const int stride = gridDim.x * kWarps, tokens = (int)a.tokens;
+  const long long gstep = (long long)a.N * D;  // from head to head in g
+  Pair w[4], dw[4];
+  load_weight(side.x.w, sub, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  for (long long token = (long long)blockIdx.x * kWarps + warp; token < a.tokens;
-       token += (long long)gridDim.x * kWarps) {
-    const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
+  for (int m = 0; m < 4; ++m) dw[m] = 0ull;
+
+  // Where the next loads come from: a token and running pointers over its
+  // heads (64-bit products and divisions only where the token changes).
+  int ft = blockIdx.x * kWarps + warp, fh = 0;
+  const TX* px = nullptr;
+  const TG* pg = nullptr;
+  const float* ps = nullptr;
+  auto aim = [&]() {
+    const int b = ft / a.N, n = ft - b * a.N;
+    fh = ha + slot;
+    px = side.x.x + b * side.x.b + n * side.x.n + fh * side.x.h + 8 * sub;
+    pg = side.g + ((long long)b * heads + fh) * gstep + (long long)n * D + 8 * sub;
+    if (sizeof(TX) == 1) ps = side.x.xs + (long long)ft * heads + fh;
+  };
+  const uint32_t ring0 = shared_at(ring + threadIdx.x);
+  uint32_t fs = 0, rs = 0;  // steps fetched and taken so far
+  if (ft < tokens) aim();
+  auto fetch_step = [&]() {
+    if (ft < tokens) {
+      if (fh < hz) {  // (a lane past the heads leaves its slots as they are)
+        const uint32_t to = ring0 + (fs % kDepth) * (SLOTS * kThreads * 16);
+        fetch_async(to, px, ps);
+        fetch_async(to + SX * kThreads * 16, pg, nullptr);
+      }
+      ++fs;
+      fh += RPW;
+      px += RPW * side.x.h;
+      pg += RPW * gstep;
+      ps += RPW;
+      if (fh - slot >= hz) {
+        ft += stride;
+        if (ft < tokens) aim();
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (uint32_t i = 0; i < kDepth - 1; ++i) fetch_step();
+
+  for (int token = blockIdx.x * kWarps + warp; token < tokens; token += stride) {
+    const int b = token / a.N, n = token - b * a.N;
+    TG* dx = side.d + b * side.b + n * side.n + (ha + slot) * side.h + 8 * sub;
     Turn<D, HALVES> turn;
-    float w[8];
-    for (int st = s0; st < s1; ++st) {
-      const bool is_k = st >= steps_q;
-      const Side<TX>& side = is_k ? a.k : a.q;
-      const TG* gy = is_k ? a.gk : a.gq;
-      const int heads = side.heads, h0 = (is_k ? st - steps_q : st) * kStep + slot;
-      Raw<TX> raw[UNROLL];
-      Raw<TG> grad[UNROLL];
+    turn.load(a.rope, b, n, sub, a.err);
+    turn.reverse();
+    for (int h = ha + slot; h - slot < hz; h += RPW) {
+      fetch_step();
+      copy_wait<kDepth - 1>();
+      const uint4* from = ring + (rs % kDepth) * (SLOTS * kThreads) + threadIdx.x;
+      ++rs;
+      Raw<TX> raw;
+      Raw<TG> grad;
+      read_slot(from, raw);
+      read_slot(from + SX * kThreads, grad);
+      const bool in = h < hz;
+      Pair x[4], g[4], ss = 0ull, dot = 0ull;
+      values(raw, x);
+      values(grad, g);
+      turn.apply(g);
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int h = min(h0 + u * RPW, heads - 1);
-        fetch(side, b, n, h, a.N, sub, raw[u]);
-        load8(gy + (((long long)b * heads + h) * a.N + n) * D + 8 * sub, grad[u]);
+      for (int m = 0; m < 4; ++m) {
+        ss = fma_f32x2(x[m], x[m], ss);
+        dot = fma_f32x2(mul_f32x2(g[m], w[m]), x[m], dot);
       }
-      if (st == s0) turn.load(a.rope, b, n, sub, a.err);
-      if (st == s0 || st == steps_q) load_weight(side.w, sub, w);
+      // both sums in one round of shuffles; mean(g w h) = r mean(g w x)
+      float s1 = added(ss), s2 = added(dot);
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int h = h0 + u * RPW;
-        float x[8], g[8];
-        values8(raw[u], x);
-        values8(grad[u], g);
-        turn.template apply<true>(g, sub);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(row_sum<TPR>(ss) * (1.0f / D) + a.eps);
-        float m = 0.f;
-        const bool in = h < heads;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= r;
-          const float gh = in ? g[e] * x[e] : 0.f;
-          if (is_k) dwk[e] += gh; else dwq[e] += gh;
-          g[e] *= w[e];
-          m = fmaf(g[e], x[e], m);
-        }
-        m = row_sum<TPR>(m) * (1.0f / D);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = r * fmaf(-x[e], m, g[e]);
-        if (in) {
-          TG* d = is_k ? a.dk + b * a.dkb + n * a.dkn + h * a.dkh : a.dq + b * a.dqb + n * a.dqn + h * a.dqh;
-          store8(d + 8 * sub, x);
-        }
+      for (int o = 1; o < TPR; o <<= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
       }
+      // (8-bit rows: x holds the codes, the row is scale * x)
+      const float scale = scale_of(raw);
+      const float r = rsqrtf(scale * scale * s1 * (1.0f / D) + a.eps);
+      const Pair r2 = both(r), h1 = both(scale * r), m2 = both(-r * r * (scale * s2 * (1.0f / D)));
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const Pair h2 = mul_f32x2(x[m], h1);
+        const Pair gh = fma_f32x2(g[m], h2, dw[m]);
+        if (in) dw[m] = gh;  // a lane past the heads adds nothing
+        x[m] = fma_f32x2(mul_f32x2(g[m], w[m]), r2, mul_f32x2(h2, m2));
+      }
+      if (in) store(dx, x);
+      dx += RPW * side.h;
     }
   }
+  copy_wait<0>();
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) red[warp * RPW + slot][8 * sub + e] = side ? dwk[e] : dwq[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float sum = 0.f;
+  for (int m = 0; m < 4; ++m) {
+    float lo, hi;
+    unpack_f32x2(dw[m], lo, hi);
+    red[warp * RPW + slot][8 * sub + 2 * m] = lo;
+    red[warp * RPW + slot][8 * sub + 2 * m + 1] = hi;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.f;
 #pragma unroll 4
-      for (int i = 0; i < kWarps * RPW; ++i) sum += red[i][threadIdx.x];
-      a.part[((long long)(blockIdx.y * gridDim.x + blockIdx.x) * 2 + side) * D + threadIdx.x] = sum;
-    }
-    __syncthreads();
+    for (int i = 0; i < kWarps * RPW; ++i) sum += red[i][threadIdx.x];
+    a.part[((long long)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = sum;
   }
 }
 
-// dw [2][D] from the CTAs' shares: thread (column, part) adds every
-// (blockDim / (2 D))-th share in order, then the parts are added in order.
+// dwq (block 0) or dwk (block 1) from the CTAs' shares: thread (column, p)
+// adds every (1024 / D)-th share in order, then the p sums are added in order.
 __global__ void __launch_bounds__(1024)
-weight_grad_kernel(const float* __restrict__ part, int ctas, int D, float* __restrict__ dwq,
+weight_grad_kernel(const float* __restrict__ part, int ctas_q, int ctas_k, int D, float* __restrict__ dwq,
                    float* __restrict__ dwk) {
   __shared__ float red[1024];
-  const int cols = 2 * D, col = threadIdx.x % cols, p = threadIdx.x / cols, parts = blockDim.x / cols;
+  const float* p0 = blockIdx.x ? part + (long long)ctas_q * D : part;
+  const int ctas = blockIdx.x ? ctas_k : ctas_q, col = threadIdx.x % D, p = threadIdx.x / D, parts = 1024 / D;
   float sum = 0.f;
 #pragma unroll 4
-  for (int i = p; i < ctas; i += parts) sum += part[(long long)i * cols + col];
+  for (int i = p; i < ctas; i += parts) sum += p0[(long long)i * D + col];
   red[threadIdx.x] = sum;
   __syncthreads();
   if (p == 0) {
-    for (int i = 1; i < parts; ++i) sum += red[i * cols + col];
-    float* dw = col < D ? dwq : dwk;
-    if (dw) dw[col % D] = sum;
+    for (int i = 1; i < parts; ++i) sum += red[i * D + col];
+    float* dw = blockIdx.x ? dwk : dwq;
+    if (dw) dw[col] = sum;
   }
 }
 
@@ -359,38 +457,48 @@ cudaError_t fwd_from8(const NormRopeFwd& f, cudaStream_t s) {
   return f.halves ? fwd_t<int8_t, TOut, 128, true, false>(f, s) : fwd_t<int8_t, TOut, 128, false, false>(f, s);
 }
 
-struct BwdGrid { int x, y; };
-
-// The persistent grid: at most kNormRopeBwdCtas CTAs, no more than the
-// tokens (times the parts of the heads, where the tokens are few) can use.
-BwdGrid bwd_grid(long long tokens, int Hq, int Hk) {
-  const int gx = (int)std::min<long long>((tokens + kWarps - 1) / kWarps, kNormRopeBwdCtas);
-  const int gy = std::max(1, std::min((Hq + 7) / 8 + (Hk + 7) / 8, kNormRopeBwdCtas / gx));
-  return {gx, gy};
-}
+// Heads per part and CTAs over the tokens: parts as long as the smaller side,
+// shorter ones while the tokens leave SMs idle, and at most kNormRopeBwdCtas
+// CTAs in all: as many as run at once (four a step apart cost a quarter of the
+// rate: registers spilled and a second wave).
+struct BwdGrid {
+  int heads, parts_q, parts_k, x;
+  BwdGrid(long long tokens, int Hq, int Hk, int step) {
+    const long long rows = (tokens + kWarps - 1) / kWarps;
+    heads = std::max(step, std::min(Hq, Hk));
+    while (heads > step && rows * (ceil_div(Hq, heads) + ceil_div(Hk, heads)) < kNormRopeBwdCtas)
+      heads = std::max(step, heads / 2);
+    // (no more parts than CTAs)
+    while (ceil_div(Hq, heads) + ceil_div(Hk, heads) > kNormRopeBwdCtas) heads *= 2;
+    parts_q = ceil_div(Hq, heads);
+    parts_k = ceil_div(Hk, heads);
+    x = (int)std::min<long long>(rows, std::max(1, kNormRopeBwdCtas / (parts_q + parts_k)));
+  }
+};
 
 template <typename TX, typename TG, int D, bool HALVES>
 cudaError_t bwd_t(const NormRopeBwd& f, cudaStream_t s) {
   BwdArgs<TX, TG> a;
-  a.q = {static_cast<const TX*>(f.xq), f.xq_scale, f.qb, f.qn, f.qh, f.Hq, f.wq};
-  a.k = {static_cast<const TX*>(f.xk), f.xk_scale, f.kb, f.kn, f.kh, f.Hk, f.wk};
-  a.gq = static_cast<const TG*>(f.gq);
-  a.gk = static_cast<const TG*>(f.gk);
-  a.dq = static_cast<TG*>(f.dxq);
-  a.dk = static_cast<TG*>(f.dxk);
-  a.dqb = f.dqb; a.dqn = f.dqn; a.dqh = f.dqh;
-  a.dkb = f.dkb; a.dkn = f.dkn; a.dkh = f.dkh;
+  a.q = {{static_cast<const TX*>(f.xq), f.xq_scale, f.qb, f.qn, f.qh, f.Hq, f.wq},
+         static_cast<const TG*>(f.gq), static_cast<TG*>(f.dxq), f.dqb, f.dqn, f.dqh};
+  a.k = {{static_cast<const TX*>(f.xk), f.xk_scale, f.kb, f.kn, f.kh, f.Hk, f.wk},
+         static_cast<const TG*>(f.gk), static_cast<TG*>(f.dxk), f.dkb, f.dkn, f.dkh};
   a.part = f.part;
   a.N = f.N;
   a.tokens = (long long)f.B * f.N;
   a.eps = f.eps;
   a.rope = f.rope;
   a.err = f.err;
-  const BwdGrid g = bwd_grid(a.tokens, f.Hq, f.Hk);
-  qk_norm_rope_bwd_kernel<TX, TG, D, HALVES, 2><<<dim3(g.x, g.y), kThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const BwdGrid g(a.tokens, f.Hq, f.Hk, 32 / (D / 8));
+  a.parts_q = g.parts_q;
+  a.heads_per_part = g.heads;
+  const int smem = (int)kDepth * bwd_slots<TX, TG>() * kThreads * 16;
+  cudaError_t e = cudaFuncSetAttribute(qk_norm_rope_bwd_kernel<TX, TG, D, HALVES>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  weight_grad_kernel<<<1, 1024, 0, s>>>(f.part, g.x * g.y, D, f.dwq, f.dwk);
+  qk_norm_rope_bwd_kernel<TX, TG, D, HALVES><<<dim3(g.x, g.parts_q + g.parts_k), kThreads, smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  weight_grad_kernel<<<2, 1024, 0, s>>>(f.part, g.x * g.parts_q, g.x * g.parts_k, D, f.dwq, f.dwk);
   return cudaGetLastError();
 }
 

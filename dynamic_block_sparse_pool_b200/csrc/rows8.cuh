@@ -14,9 +14,26 @@
 #pragma once
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 namespace rows8 {
+
+// A thread's eight values as four packed pairs: sm_100's fp32x2 instructions
+// halve the issue slots, which bound these kernels as much as memory does.
+typedef uint64_t Pair;
+__device__ __forceinline__ Pair pair(float lo, float hi) { return pack_f32x2(lo, hi); }
+__device__ __forceinline__ Pair both(float v) { return pack_f32x2(v, v); }
+__device__ __forceinline__ Pair swapped(Pair p) {
+  float a, b;
+  unpack_f32x2(p, a, b);
+  return pack_f32x2(b, a);
+}
+__device__ __forceinline__ float added(Pair p) {
+  float a, b;
+  unpack_f32x2(p, a, b);
+  return a + b;
+}
 
 // What a load of eight values brings in, before it is converted.
 template <typename T> struct Raw;
@@ -36,41 +53,77 @@ __device__ __forceinline__ void load8(const int8_t* p, Raw<int8_t>& r) {
   r.v = __ldcs(reinterpret_cast<const uint2*>(p));
 }
 
-__device__ __forceinline__ void unpack_bf16(uint32_t w, float& lo, float& hi) {
-  lo = __uint_as_float(w << 16);
-  hi = __uint_as_float(w & 0xffff0000u);
+__device__ __forceinline__ Pair unpack_bf16(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ void values8(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
-  unpack_bf16(r.v.x, x[0], x[1]);
-  unpack_bf16(r.v.y, x[2], x[3]);
-  unpack_bf16(r.v.z, x[4], x[5]);
-  unpack_bf16(r.v.w, x[6], x[7]);
+__device__ __forceinline__ void values(const Raw<__nv_bfloat16>& r, Pair (&x)[4]) {
+  x[0] = unpack_bf16(r.v.x);
+  x[1] = unpack_bf16(r.v.y);
+  x[2] = unpack_bf16(r.v.z);
+  x[3] = unpack_bf16(r.v.w);
 }
-__device__ __forceinline__ void values8(const Raw<float>& r, float (&x)[8]) {
-  x[0] = __uint_as_float(r.v.x); x[1] = __uint_as_float(r.v.y);
-  x[2] = __uint_as_float(r.v.z); x[3] = __uint_as_float(r.v.w);
-  x[4] = __uint_as_float(r.w.x); x[5] = __uint_as_float(r.w.y);
-  x[6] = __uint_as_float(r.w.z); x[7] = __uint_as_float(r.w.w);
+__device__ __forceinline__ void values(const Raw<float>& r, Pair (&x)[4]) {
+  x[0] = pair(__uint_as_float(r.v.x), __uint_as_float(r.v.y));
+  x[1] = pair(__uint_as_float(r.v.z), __uint_as_float(r.v.w));
+  x[2] = pair(__uint_as_float(r.w.x), __uint_as_float(r.w.y));
+  x[3] = pair(__uint_as_float(r.w.z), __uint_as_float(r.w.w));
 }
-__device__ __forceinline__ void values8(const Raw<int8_t>& r, float (&x)[8]) {
+// The codes, without their scale, and without a conversion instruction (they
+// run at an eighth of the FMA rate): the byte c + 128 as the low mantissa byte
+// of 2^23 is the float 2^23 + 128 + c; subtracting 2^23 + 128 is exact.
+__device__ __forceinline__ void values(const Raw<int8_t>& r, Pair (&x)[4]) {
+  const uint32_t w[2] = {r.v.x ^ 0x80808080u, r.v.y ^ 0x80808080u};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[e] = (float)(int8_t)(r.v.x >> (8 * e)) * r.scale;
-    x[4 + e] = (float)(int8_t)(r.v.y >> (8 * e)) * r.scale;
+  for (int m = 0; m < 4; ++m) {
+    const uint32_t v = w[m >> 1], k = 2 * (m & 1);
+    x[m] = add_f32x2(pair(__uint_as_float(__byte_perm(v, 0x4b000000u, 0x7440u + k)),
+                          __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7441u + k))), both(-8388736.0f));
   }
 }
+// What the values have to be multiplied by.
+template <typename T>
+__device__ __forceinline__ float scale_of(const Raw<T>&) { return 1.f; }
+__device__ __forceinline__ float scale_of(const Raw<int8_t>& r) { return r.scale; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint32_t pack_bf16(Pair p) {
+  float a, b;
+  unpack_f32x2(p, a, b);
+  return pack_bf16(a, b);
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store(__nv_bfloat16* p, const Pair (&x)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0]), pack_bf16(x[1]), pack_bf16(x[2]), pack_bf16(x[3]));
+}
+__device__ __forceinline__ void store(float* p, const Pair (&x)[4]) {
+  float v[8];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) unpack_f32x2(x[m], v[2 * m], v[2 * m + 1]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// The same loads into shared memory, asynchronously (16-byte slots, one or two
+// per load, kThreads apart): what is in flight costs no registers, and as
+// every thread reads back only its own slots, no barrier is needed.
+template <typename T> struct Slots { static constexpr int kCount = sizeof(T) == 4 ? 2 : 1; };
+
+__device__ __forceinline__ uint32_t shared_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 // Sum over the TPR (8 or 16) neighbouring threads of a row, in all of them.
@@ -81,12 +134,22 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// Bits of the largest magnitude of eight values (integer order is the order
+// of magnitudes, NaN above infinity).
+__device__ __forceinline__ uint32_t top_bits(const Raw<__nv_bfloat16>& r) {
+  constexpr uint32_t kMag = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(r.v.x & kMag, r.v.y & kMag), __vmaxu2(r.v.z & kMag, r.v.w & kMag));
+  return max(m << 16, m & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t top_bits(const Raw<float>& r) {
+  constexpr uint32_t kMag = 0x7fffffffu;
+  return max(max(max(r.v.x & kMag, r.v.y & kMag), max(r.v.z & kMag, r.v.w & kMag)),
+             max(max(r.w.x & kMag, r.w.y & kMag), max(r.w.z & kMag, r.w.w & kMag)));
+}
+
 // The row's codes and scale from its threads' values (see above).
 template <int TPR>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float& scale) {
-  uint32_t top = 0;  // magnitude bits: integer order is the order of magnitudes
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+__device__ __forceinline__ uint2 encode8(const Pair (&x)[4], uint32_t top, float& scale) {
 #pragma unroll
   for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float amax = __uint_as_float(top);
@@ -98,11 +161,19 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float& scale) {
     scale = __fdiv_rn(amax, 127.0f);
     inv = __fdiv_rn(127.0f, amax);
   }
-  uint32_t w[2] = {0u, 0u};
+  // round-half-even by the adder: 1.5 * 2^23 + v keeps the integer nearest to v
+  // (ties to even) in its low bits, here the low byte as |v| <= 127
+  uint32_t t[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    w[e >> 2] |= ((uint32_t)__float2int_rn(__fmul_rn(x[e], inv)) & 0xffu) << (8 * (e & 3));
-  return make_uint2(w[0], w[1]);
+  for (int m = 0; m < 4; ++m) {
+    float a, b;  // (not packed: the product has to be rounded before the sum)
+    unpack_f32x2(x[m], a, b);
+    t[2 * m] = __float_as_uint(__fadd_rn(__fmul_rn(a, inv), 12582912.0f));
+    t[2 * m + 1] = __float_as_uint(__fadd_rn(__fmul_rn(b, inv), 12582912.0f));
+  }
+  return make_uint2(
+      __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
 }
 
 }  // namespace rows8

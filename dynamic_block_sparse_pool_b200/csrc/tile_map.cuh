@@ -1,6 +1,5 @@
-// Tensor maps of [heads, N, D] bf16 arrays read or written as tiles of
-// 64 columns x 128 rows in the 128-byte-swizzled shared-memory layout.
-// Rows past N read as zeros and are not written.
+// Tensor maps of bf16 arrays, read as tiles in the 128-byte-swizzled
+// shared-memory layout.  Places outside the tensor read as zeros.
 #pragma once
 
 #include <cuda.h>
@@ -8,7 +7,10 @@
 
 namespace dsa {
 
-inline bool make_bf16_tile_map(CUtensorMap* map, const void* ptr, int heads, int N, int D) {
+// A bf16 tensor of 3 or 4 dimensions (strides of all but the first, in bytes),
+// read in boxes in the 128-byte-swizzled layout.
+inline bool encode_bf16_map(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
+                            const cuuint64_t* strides, const cuuint32_t* box) {
   typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -23,13 +25,18 @@ inline bool make_bf16_tile_map(CUtensorMap* map, const void* ptr, int heads, int
     return reinterpret_cast<Encode>(p);
   }();
   if (!fn) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [heads, N, D] in tiles of 64 columns x 128 rows.
+inline bool make_bf16_tile_map(CUtensorMap* map, const void* ptr, int heads, int N, int D) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)heads};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
   const cuuint32_t box[3] = {64, 128, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bf16_map(map, ptr, 3, dims, strides, box);
 }
 
 }  // namespace dsa

@@ -29,11 +29,20 @@ struct DecodeAttn {
   const int32_t* lens;        // [B]: keys in the cache, the new tokens' among them
   void* out;                  // [B, H, Nq, D]
   float* lse;                 // [B, H, Nq], NULL if not wanted
-  int num_sms;
+  int groups;                 // CTAs per head that join through the workspace
+  float* ws;                  // [groups][B H Nq][D], then [groups][B H Nq] (maximum, sum)
   unsigned* err;
 };
 
-cudaError_t launch_window_decode(const DecodeAttn& a, bool bf16, int D, cudaStream_t s);
+// How the keys of one head are shared: `cluster` CTAs that join on the SMs, or
+// `groups` that join through the workspace (one of the two is 1).
+struct DecodePlan {
+  int tiles, cluster, groups;  // tiles: of a group's rows
+};
+DecodePlan decode_plan(bool bf16, int B, int H, int Hk, int Nq, int cap, int D, int left, int sink);
+
+cudaError_t launch_window_decode(const DecodeAttn& a, const DecodePlan& plan, bool bf16, int D, cudaStream_t s,
+                                 const char** why);
 
 // bf16 on tcgen05
 cudaError_t launch_window_fwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why);

@@ -623,7 +623,8 @@ def window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
 
 def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
                        left: int = -1, sink: int = 0, scale: Optional[float] = None,
-                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """O [B, H, Nq, D] of each stream's newest Nq tokens (up to 128) over its
     cache: window_attn_fwd with right = 0 and q_offset = lens[b] - Nq.
 
@@ -646,11 +647,16 @@ def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     _check_lse(lse, q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     st6 = _strides6(*([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k_cache, v_cache)))
+    Hk, cap, dt = k_cache.shape[1], k_cache.shape[2], _dtype_code(q)
+    if workspace is None:
+        n = int(lib().dsa_window_attn_decode_workspace_size(dt, B, H, Hk, Nq, cap, D, int(left), int(sink)))
+        workspace = torch.empty(n, device=q.device, dtype=torch.uint8) if n else None
     with torch.cuda.device(q.device):
         st = lib().dsa_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), st6.data_ptr(),
-                                          _dtype_code(q), B, H, k_cache.shape[1], Nq, k_cache.shape[2], D,
-                                          scale, lens.data_ptr(), int(left), int(sink), out.data_ptr(),
-                                          _ptr(lse), _stream(q))
+                                          dt, B, H, Hk, Nq, cap, D, scale, lens.data_ptr(), int(left),
+                                          int(sink), out.data_ptr(), _ptr(lse), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                          _stream(q))
     check(st, "dsa_window_attn_decode")
     return out
 

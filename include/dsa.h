@@ -488,7 +488,7 @@ dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table);
  * Statistics and rotation are in fp32; each output is rounded once.
  * Errors: DSA_ERR_INVALID_ARG as listed; a position at or past its axis'
  * length sets the device error word and does not turn.  Outputs must not
- * overlap inputs.  Limits: D 64 or 128; B*N < 2^31; Hq, Hk 1..65535.
+ * overlap inputs.  Limits: D 64 or 128; B*N < 2^31 - 65536; Hq, Hk 1..65535.
  */
 dsa_status dsa_qk_norm_rope(const void* xq, const void* xk, const float* xq_scale,
                             const float* xk_scale, const int64_t* x_strides, dsa_dtype dt, int B,
@@ -587,13 +587,17 @@ size_t dsa_window_attn_bwd_workspace_size(int B, int H, int Nq);
  *   q         [B, H, Nq, D] in dt, contiguous;  Nq 1 .. 128.
  *   k, v      caches [B, Hk, cap, D] in dt, read through `kv_strides` (host,
  *             int64 [6]: k's strides of b, h, n, then v's, in elements; D
- *             contiguous, strides multiples of 16 bytes).
+ *             contiguous, strides multiples of 16 bytes, at least D and below
+ *             2^38 where the dimension is above 1).
  *   lens      device, int32 [B]: the keys in each stream's cache, the Nq new
  *             ones among them; query i stands at position lens[b] - Nq + i.
  *             A query at a negative position sees nothing (o = 0, lse = -inf).
  *   left, sink, out, lse  as in dsa_window_attn_fwd.
- * Cache rows that no query sees are not read.  One launch, no workspace; lens
- * is read on the device, so a captured call serves a growing cache.
+ *   workspace >= dsa_window_attn_decode_workspace_size(...) bytes, 16-byte
+ *             aligned; may be NULL where that is 0.  Calls that may run at the
+ *             same time need workspaces of their own.
+ * What cache rows that no query sees hold does not matter.  lens is read on
+ * the device, so a captured call serves a growing cache.
  * Errors: DSA_ERR_INVALID_ARG as listed; a length outside [0, cap] sets the
  * device error word and is taken as 0.
  * Limits: D 64 or 128; B*H <= 65535; cap 1 .. 2^27; sink >= 0.
@@ -601,7 +605,13 @@ size_t dsa_window_attn_bwd_workspace_size(int B, int H, int Nq);
 dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
                                   const int64_t* kv_strides, dsa_dtype dt, int B, int H, int Hk,
                                   int Nq, int cap, int D, float scale, const int32_t* lens,
-                                  int left, int sink, void* out, float* lse, void* stream);
+                                  int left, int sink, void* out, float* lse, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/* Device workspace bytes for dsa_window_attn_decode with these arguments (0
+ * where the call needs none, and for invalid sizes). */
+size_t dsa_window_attn_decode_workspace_size(dsa_dtype dt, int B, int H, int Hk, int Nq, int cap,
+                                             int D, int left, int sink);
 
 /*
  * Activation rows kept in 8 bits between the forward and the backward.  (No

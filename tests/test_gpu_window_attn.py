@@ -256,6 +256,8 @@ CACHES = [
     (1, 2, 2, 1, 5000, 128, -1, 0, [4999]),            # a cluster shares one head
     (2, 3, 3, 2, 4100, 64, 4000, 130, [4100, 3000]),
     (1, 2, 1, 1, 2000, 128, 0, 1, [2000]),
+    (1, 4, 2, 2, 33000, 128, -1, 0, [32999]),          # large enough for shares through the workspace
+    (2, 2, 2, 1, 40000, 64, 30000, 300, [40000, 31]),
 ]
 
 
