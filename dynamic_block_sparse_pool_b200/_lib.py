@@ -39,7 +39,7 @@ SIGNATURES = {
     "dsa_hilbert_order": (_i, [_i, _i, _i, _i, _vp]),
     "dsa_gilbert_order": (_i, [_i, _i, _i, _i, _vp]),
     "dsa_permute_tokens": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
-    "dsa_rope_table": (_i, [_i, _i, _f, _vp]),
+    "dsa_rope_table": (_i, [_i, _i, _f, _vp, _vp]),
     "dsa_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _f, _vp, _vp,
                               _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "dsa_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp,
@@ -50,7 +50,7 @@ SIGNATURES = {
                                  _vp, _vp]),
     "dsa_window_attn_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i,
                                  _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
-    "dsa_window_attn_bwd_workspace_size": (_sz, [_i, _i, _i]),
+    "dsa_window_attn_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "dsa_window_attn_decode": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _i,
                                     _vp, _vp, _vp, _sz, _vp]),
     "dsa_window_attn_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),

@@ -115,8 +115,8 @@ dsa_status check_heads(int B, int H, int Hk, int D, float scale, int sink, dsa_d
 int bound(int v) { return v < 0 || v > dsa::Window::kNoBound ? dsa::Window::kNoBound : v; }
 
 // Checks and arguments that the window attention's passes share.
-dsa_status window_args(dsa::WindowAttn& a, const void* q, const void* k, const void* v, dsa_dtype dt, int B, int H,
-                       int Hk, int Nq, int Nk, int D, float scale, int q_offset, int left, int right, int sink) {
+dsa_status window_shape(dsa::WindowAttn& a, dsa_dtype dt, int B, int H, int Hk, int Nq, int Nk, int D, float scale,
+                        int q_offset, int left, int right, int sink) {
   dsa_status st = check_heads(B, H, Hk, D, scale, sink, dt);
   if (st != DSA_OK) return st;
   if (Nq < 1 || Nk < 1 || Nq > (1 << 27) || Nk > (1 << 27))
@@ -125,15 +125,28 @@ dsa_status window_args(dsa::WindowAttn& a, const void* q, const void* k, const v
     return fail(DSA_ERR_INVALID_ARG, "q_offset must be within 2^28 of 0 (got %d)", q_offset);
   const long long tiles = (std::max(Nq, Nk) + 63ll) / 64;
   if ((long long)B * H * tiles > INT_MAX) return fail(DSA_ERR_INVALID_ARG, "too many query or key tiles");
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
-    return fail(DSA_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
   a = {};
   a.B = B; a.H = H; a.Hk = Hk; a.D = D;
   a.w = {Nq, Nk, q_offset, bound(left), bound(right), std::min(sink, Nk)};
   a.scale = scale;
+  return DSA_OK;
+}
+
+dsa_status window_args(dsa::WindowAttn& a, const void* q, const void* k, const void* v, dsa_dtype dt, int B, int H,
+                       int Hk, int Nq, int Nk, int D, float scale, int q_offset, int left, int right, int sink) {
+  dsa_status st = window_shape(a, dt, B, H, Hk, Nq, Nk, D, scale, q_offset, left, right, sink);
+  if (st != DSA_OK) return st;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
   a.q = q; a.k = k; a.v = v;
   if ((st = dsa::api_checked_device(&a.err)) != DSA_OK) return st;
   return sm_count(&a.num_sms);
+}
+
+size_t delta_bytes(const dsa::WindowAttn& a) { return ((size_t)a.B * a.H * a.w.Nq * sizeof(float) + 15) / 16 * 16; }
+
+size_t window_bwd_bytes(const dsa::WindowAttn& a, dsa_dtype dt) {
+  return delta_bytes(a) + (dt == DSA_F32 ? dsa::simt_share_floats(a.B, a.H, a.Hk, a.w, a.D) * sizeof(float) : 0);
 }
 
 }  // namespace
@@ -160,9 +173,12 @@ dsa_status dsa_window_attn_fwd(const void* q, const void* k, const void* v, dsa_
   return launched(e, "window_attn_fwd launch");
 }
 
-size_t dsa_window_attn_bwd_workspace_size(int B, int H, int Nq) {
-  if (B < 1 || H < 1 || Nq < 1) return 0;
-  return ((size_t)B * H * Nq * sizeof(float) + 15) / 16 * 16;
+size_t dsa_window_attn_bwd_workspace_size(dsa_dtype dt, int B, int H, int Hk, int Nq, int Nk, int D, int q_offset,
+                                          int left, int right, int sink) {
+  dsa::api_set_last_error("");
+  dsa::WindowAttn a;
+  if (window_shape(a, dt, B, H, Hk, Nq, Nk, D, 1.f, q_offset, left, right, sink) != DSA_OK) return 0;
+  return window_bwd_bytes(a, dt);
 }
 
 dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
@@ -179,13 +195,14 @@ dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, cons
   dsa::WindowAttn a;
   dsa_status st = window_args(a, q, k, v, dt, B, H, Hk, Nq, Nk, D, scale, q_offset, left, right, sink);
   if (st != DSA_OK) return st;
-  if (ws_bytes < dsa_window_attn_bwd_workspace_size(B, H, Nq))
+  if (ws_bytes < window_bwd_bytes(a, dt))
     return fail(DSA_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu needed", ws_bytes,
-                dsa_window_attn_bwd_workspace_size(B, H, Nq));
+                window_bwd_bytes(a, dt));
   a.o = out; a.dout = dout;
   a.lse = const_cast<float*>(lse);
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.delta = static_cast<float*>(workspace);
+  a.shares = a.delta + delta_bytes(a) / sizeof(float);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const char* why = nullptr;
   cudaError_t e = dsa::launch_row_delta(out, dout, dt == DSA_BF16, (long long)B * H * Nq, D, a.delta, s);
@@ -260,21 +277,19 @@ dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
   return launched(e, "window_attn_decode launch");
 }
 
-dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table) {
+dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table, void* stream) {
   dsa::api_set_last_error("");
   if (!table) return fail(DSA_ERR_INVALID_ARG, "null table");
   if (positions < 1 || pairs < 1 || pairs > 64)
     return fail(DSA_ERR_INVALID_ARG, "need positions >= 1 and pairs in 1..64 (got %d, %d)", positions, pairs);
   if ((long long)positions * pairs > (1 << 30)) return fail(DSA_ERR_INVALID_ARG, "the table exceeds 2^30 entries");
   if (!(theta > 0.f) || !std::isfinite(theta)) return fail(DSA_ERR_INVALID_ARG, "theta must be finite and > 0");
-  for (int i = 0; i < pairs; ++i) {
-    const double f = std::pow((double)theta, -(double)i / pairs);
-    for (long long p = 0; p < positions; ++p) {
-      table[(p * pairs + i) * 2] = (float)std::cos((double)p * f);
-      table[(p * pairs + i) * 2 + 1] = (float)std::sin((double)p * f);
-    }
-  }
-  return DSA_OK;
+  if (!aligned(table, 8)) return fail(DSA_ERR_INVALID_ARG, "table must be 8-byte aligned");
+  unsigned* err = nullptr;
+  const dsa_status st = dsa::api_checked_device(&err);
+  if (st != DSA_OK) return st;
+  return launched(dsa::launch_rope_table(positions, pairs, theta, reinterpret_cast<float2*>(table),
+                                         static_cast<cudaStream_t>(stream)), "rope_table launch");
 }
 
 dsa_status dsa_qk_norm_rope(const void* xq, const void* xk, const float* xq_scale,

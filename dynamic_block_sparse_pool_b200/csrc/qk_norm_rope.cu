@@ -408,6 +408,17 @@ weight_grad_kernel(const float* __restrict__ part, int ctas_q, int ctas_k, int D
   }
 }
 
+// One axis' table in 64 bits: grid x over positions, one thread per pair.
+__global__ void rope_table_kernel(int positions, int pairs, double theta, float2* __restrict__ table) {
+  const int i = threadIdx.x;
+  const double f = pow(theta, -(double)i / pairs);
+  for (int p = blockIdx.x * blockDim.y + threadIdx.y; p < positions; p += gridDim.x * blockDim.y) {
+    double s, c;
+    sincos(p * f, &s, &c);
+    table[(long long)p * pairs + i] = make_float2((float)c, (float)s);
+  }
+}
+
 template <typename TIn, typename TOut, int D, bool HALVES, bool SAVE8>
 cudaError_t fwd_t(const NormRopeFwd& f, cudaStream_t s) {
   constexpr int RPW = 32 / (D / 8);
@@ -509,6 +520,13 @@ cudaError_t bwd_dispatch(const NormRopeBwd& f, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_rope_table(int positions, int pairs, float theta, float2* table, cudaStream_t s) {
+  const dim3 block((unsigned)pairs, (unsigned)std::max(1, 128 / pairs));
+  rope_table_kernel<<<(unsigned)std::min(ceil_div(positions, (int)block.y), 2048), block, 0, s>>>(positions, pairs, theta,
+                                                                                              table);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_qk_norm_rope(const NormRopeFwd& f, cudaStream_t s) {
   if (f.xq_scale)

@@ -73,6 +73,9 @@ struct QueryRun {
     const int b = k0 < w.sink ? w.Nq : Window::min_(w.Nq, k1 - 1 + w.left - w.off + 1);
     return {a, Window::max_(a, b)};
   }
+  // tiles of BM queries that the run touches
+  template <int BM>
+  __host__ __device__ int tiles() const { return q1 > q0 ? (q1 + BM - 1) / BM - q0 / BM : 0; }
 };
 
 // Whether every query of [q0, q1) sees every key of [k0, k1).

@@ -16,6 +16,7 @@ struct WindowAttn {
   const void *o, *dout;       // the forward's output and its gradient
   void *dq, *dk, *dv;
   float* delta;               // workspace, [B, H, Nq]
+  float* shares;              // workspace, simt_share_floats (fp32)
   int num_sms;
   unsigned* err;
 };
@@ -48,6 +49,12 @@ cudaError_t launch_window_decode(const DecodeAttn& a, const DecodePlan& plan, bo
 cudaError_t launch_window_fwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why);
 cudaError_t launch_window_bwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why);
 // fp32 on CUDA cores
+// Chunks of a gradient tile's pairs, and the floats their shares take.
+struct SimtChunks {
+  int chunk_q, chunks_q, chunk_k, chunks_k;
+};
+SimtChunks simt_chunks(int B, int H, int Hk, const Window& w);
+size_t simt_share_floats(int B, int H, int Hk, const Window& w, int D);
 cudaError_t launch_window_fwd_simt(const WindowAttn& a, cudaStream_t s);
 cudaError_t launch_window_bwd_simt(const WindowAttn& a, cudaStream_t s);
 

@@ -9,8 +9,11 @@
 // D + 4 (64 + 4) floats, so the 16 columns of a load fall in different banks.
 //
 // Formulas as in window_fwd_sm100.cu and window_bwd_sm100.cu.  dK and dV of a
-// key head are summed over its query heads and queries in a fixed order by
-// one CTA: no atomics, equal bits from run to run.
+// key head are summed over its query heads and queries in a fixed order, no
+// atomics: equal bits from run to run.  A tile pair takes about 5 us, so where
+// the tiles of one side are few, or one of them (a sink's) sees far more than
+// the others, a gradient tile's pairs are cut into chunks (SimtChunks), one CTA
+// each, whose partial sums a last kernel adds in order.
 #include <algorithm>
 
 #include "window_attn.cuh"
@@ -218,10 +221,10 @@ __device__ __forceinline__ void stage_vec(float* dst, const float* src, int r0, 
 
 // dQ of a query tile
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                       const float* __restrict__ dout, const float* __restrict__ lse, const float* __restrict__ delta,
-                      const Window w, int group, float scale, float* __restrict__ dq) {
+                      const Window w, int group, float scale, int chunk, float* __restrict__ dq) {
   constexpr int P = padded<D>();
   extern __shared__ __align__(16) float sm[];
   float *Q = sm, *O = Q + T * P, *K = O + T * P, *V = K + T * P, *W = V + T * P, *ls = W + T * SP, *de = ls + T;
@@ -229,13 +232,16 @@ window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, 
   const int tiles = ceil_div(w.Nq, T), bh = blockIdx.x / tiles, q0 = (blockIdx.x - bh * tiles) * T;
   const int q1 = min(q0 + T, w.Nq);
   const size_t qh = (size_t)bh * w.Nq * D, kh = (size_t)(bh / group) * w.Nk * D;
+  const KeyTiles<T> kt = KeyTiles<T>::of(w, q0, q1);
+  const int e0 = blockIdx.y * chunk, e1 = min(kt.count(), e0 + chunk);
+  if (blockIdx.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
+  dq += blockIdx.y * ((size_t)(gridDim.x / tiles) * w.Nq * D);
   stage<D>(Q, q + qh, q0, w.Nq);
   stage<D>(O, dout + qh, q0, w.Nq);
   stage_vec(ls, lse + (size_t)bh * w.Nq, q0, w.Nq, -INFINITY);
   stage_vec(de, delta + (size_t)bh * w.Nq, q0, w.Nq, 0.f);
   float acc[4][D / 16] = {};
-  const KeyTiles<T> kt = KeyTiles<T>::of(w, q0, q1);
-  for (int e = 0; e < kt.count(); ++e) {
+  for (int e = e0; e < e1; ++e) {
     const int k0 = kt.tile(e) * T;
     __syncthreads();
     stage<D>(K, k + kh, k0, w.Nk);
@@ -258,10 +264,10 @@ window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, 
 
 // dK and dV of a key tile, over the query heads of its key head
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                         const float* __restrict__ dout, const float* __restrict__ lse,
-                        const float* __restrict__ delta, const Window w, int group, float scale,
+                        const float* __restrict__ delta, const Window w, int group, float scale, int chunk,
                         float* __restrict__ dk, float* __restrict__ dv) {
   constexpr int P = padded<D>();
   extern __shared__ __align__(16) float sm[];
@@ -270,13 +276,18 @@ window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k
   const int tiles = ceil_div(w.Nk, T), kv = blockIdx.x / tiles, k0 = (blockIdx.x - kv * tiles) * T;
   const int k1 = min(k0 + T, w.Nk);
   const size_t kh = (size_t)kv * w.Nk * D;
+  const QueryRun run = QueryRun::of(w, k0, k1);
+  const int i0 = run.q0 / T, per = run.tiles<T>(), n = per * group;  // query tiles per head, head after head
+  const int e0 = blockIdx.y * chunk, e1 = min(n, e0 + chunk);
+  if (blockIdx.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
+  const size_t share = blockIdx.y * ((size_t)(gridDim.x / tiles) * w.Nk * D);
   stage<D>(K, k + kh, k0, w.Nk);
   stage<D>(V, v + kh, k0, w.Nk);
   float ak[4][D / 16] = {}, av[4][D / 16] = {};
-  const QueryRun run = QueryRun::of(w, k0, k1);
-  for (int h = 0; h < group; ++h) {
-    const size_t bh = (size_t)kv * group + h, qh = bh * w.Nq * D;
-    for (int q0 = run.q0 / T * T; q0 < run.q1; q0 += T) {
+  {
+    for (int e = e0; e < e1; ++e) {
+      const int h = e / per, q0 = (i0 + e - h * per) * T;
+      const size_t bh = (size_t)kv * group + h, qh = bh * w.Nq * D;
       __syncthreads();
       stage<D>(Q, q + qh, q0, w.Nq);
       stage<D>(O, dout + qh, q0, w.Nq);
@@ -304,8 +315,30 @@ window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k
     }
   }
   float one[4] = {1.f, 1.f, 1.f, 1.f}, mul[4] = {scale, scale, scale, scale};
-  store_rows<D>(dv + kh, av, k0, k1, one, ty, tx);
-  store_rows<D>(dk + kh, ak, k0, k1, mul, ty, tx);
+  store_rows<D>(dv + share + kh, av, k0, k1, one, ty, tx);
+  store_rows<D>(dk + share + kh, ak, k0, k1, mul, ty, tx);
+}
+
+// Sums the chunks' shares of one gradient, [chunks][heads][N][D] -> [heads][N][D];
+// a row of a tile has as many shares as the tile has chunks (at least one).
+template <int D, bool KEYS>
+__global__ void __launch_bounds__(kThreads)
+window_join_simt_kernel(const float* __restrict__ part, const Window w, int group, int chunk, long long rows,
+                        float* __restrict__ out) {
+  constexpr int V = D / 4;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, row = i / V;
+  if (row >= rows) return;
+  const int N = KEYS ? w.Nk : w.Nq, x0 = (int)(row % N) / T * T, x1 = min(x0 + T, N);
+  const int n = KEYS ? QueryRun::of(w, x0, x1).tiles<T>() * group : KeyTiles<T>::of(w, x0, x1).count();
+  const int chunks = max(1, ceil_div(n, chunk));
+  const float4* p = reinterpret_cast<const float4*>(part) + i;
+  float4 s = *p;
+  for (int c = 1; c < chunks; ++c) {
+    p += rows * V;
+    const float4 x = *p;
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  reinterpret_cast<float4*>(out)[i] = s;
 }
 
 template <int D>
@@ -329,15 +362,64 @@ cudaError_t bwd_d(const WindowAttn& a, cudaStream_t s) {
   const float *q = static_cast<const float*>(a.q), *k = static_cast<const float*>(a.k),
               *v = static_cast<const float*>(a.v), *g = static_cast<const float*>(a.dout);
   const int group = a.H / a.Hk;
-  window_dq_simt_kernel<D><<<a.B * a.H * ceil_div(a.w.Nq, T), kThreads, smem, s>>>(
-      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, static_cast<float*>(a.dq));
+  const SimtChunks c = simt_chunks(a.B, a.H, a.Hk, a.w);
+  const long long rq = (long long)a.B * a.H * a.w.Nq, rk = (long long)a.B * a.Hk * a.w.Nk;
+  // shares: dQ's, dK's, dV's, each where it has more than one
+  float* pq = c.chunks_q > 1 ? a.shares : static_cast<float*>(a.dq);
+  float* pk = c.chunks_k > 1 ? a.shares + (c.chunks_q > 1 ? c.chunks_q * rq * D : 0) : static_cast<float*>(a.dk);
+  float* pv = c.chunks_k > 1 ? pk + c.chunks_k * rk * D : static_cast<float*>(a.dv);
+  window_dq_simt_kernel<D><<<dim3((unsigned)(a.B * a.H * ceil_div(a.w.Nq, T)), (unsigned)c.chunks_q), kThreads, smem, s>>>(
+      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, c.chunk_q, pq);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  window_dkdv_simt_kernel<D><<<a.B * a.Hk * ceil_div(a.w.Nk, T), kThreads, smem, s>>>(
-      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, static_cast<float*>(a.dk), static_cast<float*>(a.dv));
+  window_dkdv_simt_kernel<D><<<dim3((unsigned)(a.B * a.Hk * ceil_div(a.w.Nk, T)), (unsigned)c.chunks_k), kThreads, smem, s>>>(
+      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, c.chunk_k, pk, pv);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  auto grid = [](long long rows) { return (unsigned)((rows * (D / 4) + kThreads - 1) / kThreads); };
+  if (c.chunks_q > 1)
+    window_join_simt_kernel<D, false><<<grid(rq), kThreads, 0, s>>>(pq, a.w, group, c.chunk_q, rq, static_cast<float*>(a.dq));
+  if (c.chunks_k > 1) {
+    window_join_simt_kernel<D, true><<<grid(rk), kThreads, 0, s>>>(pk, a.w, group, c.chunk_k, rk, static_cast<float*>(a.dk));
+    window_join_simt_kernel<D, true><<<grid(rk), kThreads, 0, s>>>(pv, a.w, group, c.chunk_k, rk, static_cast<float*>(a.dv));
+  }
   return cudaGetLastError();
 }
 
 }  // namespace
+
+// The chunks of tile pairs: as long as half an SM's share of all pairs; one
+// chunk where the longest tile is at most half as long again.
+SimtChunks simt_chunks(int B, int H, int Hk, const Window& w) {
+  auto cut = [](long long heads, int tiles, auto count, int& chunk, int& chunks) {
+    long long all = 0;
+    int longest = 1;
+    for (int t = 0; t < tiles; ++t) {
+      const int n = count(t);
+      all += n;
+      longest = std::max(longest, n);
+    }
+    const long long share = std::max(1ll, (all * heads + 295) / 296);
+    chunk = longest;
+    chunks = 1;
+    if (2ll * longest > 3 * share) {
+      chunk = (int)share;
+      chunks = ceil_div(longest, chunk);
+    }
+  };
+  SimtChunks c;
+  const int group = H / Hk;
+  cut((long long)B * H, ceil_div(w.Nq, T),
+      [&](int t) { return KeyTiles<T>::of(w, t * T, std::min((t + 1) * T, w.Nq)).count(); }, c.chunk_q, c.chunks_q);
+  cut((long long)B * Hk, ceil_div(w.Nk, T),
+      [&](int t) { return QueryRun::of(w, t * T, std::min((t + 1) * T, w.Nk)).tiles<T>() * group; }, c.chunk_k,
+      c.chunks_k);
+  return c;
+}
+
+size_t simt_share_floats(int B, int H, int Hk, const Window& w, int D) {
+  const SimtChunks c = simt_chunks(B, H, Hk, w);
+  return ((c.chunks_q > 1 ? (size_t)c.chunks_q * B * H * w.Nq : 0) +
+          (c.chunks_k > 1 ? (size_t)c.chunks_k * 2 * B * Hk * w.Nk : 0)) * D;
+}
 
 cudaError_t launch_window_fwd_simt(const WindowAttn& a, cudaStream_t s) {
   return a.D == 64 ? fwd_d<64>(a, s) : fwd_d<128>(a, s);

@@ -6,6 +6,8 @@ contiguous, bf16 or fp32, on one CUDA device.
 """
 from __future__ import annotations
 
+import contextlib
+import ctypes
 import math
 from typing import NamedTuple, Optional, Tuple
 
@@ -23,6 +25,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(t: torch.Tensor):
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _on(t: torch.Tensor):
+    """t's device as the current one."""
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -325,7 +332,7 @@ def pack8(x: torch.Tensor) -> Act8:
              torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32))
     if x.numel() == 0:
         return a
-    with torch.cuda.device(x.device):
+    with _on(x):
         st = lib().dsa_pack8(x.data_ptr(), dt, x.numel() // D, D, a.codes.data_ptr(),
                              a.scales.data_ptr(), _stream(x))
     check(st, "dsa_pack8")
@@ -343,19 +350,22 @@ def unpack8(a: Act8, dtype: torch.dtype = torch.bfloat16,
     dt, D = _dtype_code(out), out.shape[-1]
     if out.numel() == 0:
         return out
-    with torch.cuda.device(out.device):
+    with _on(out):
         st = lib().dsa_unpack8(a.codes.data_ptr(), a.scales.data_ptr(), dt, out.numel() // D, D,
                                out.data_ptr(), _stream(out))
     check(st, "dsa_unpack8")
     return out
 
 
-def rope_table(positions: int, pairs: int, theta: float = 10000.0) -> torch.Tensor:
-    """Host fp32 [positions, pairs, 2]: cos and sin of p * theta^(-i / pairs)."""
+def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None) -> torch.Tensor:
+    """fp32 [positions, pairs, 2] on the device: cos and sin of p * theta^(-i / pairs)."""
     if positions < 1 or pairs < 1:
         raise ValueError("positions and pairs must be at least 1")
-    t = torch.empty(positions, pairs, 2, dtype=torch.float32)
-    check(lib().dsa_rope_table(positions, pairs, float(theta), t.data_ptr()), "dsa_rope_table")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    t = torch.empty(positions, pairs, 2, dtype=torch.float32, device=dev)
+    with _on(t):
+        st = lib().dsa_rope_table(positions, pairs, float(theta), t.data_ptr(), _stream(t))
+    check(st, "dsa_rope_table")
     return t
 
 
@@ -389,9 +399,9 @@ class RopePlan:
         self.pairs = tuple(pairs + [0] * (3 - len(pairs)))
         self.lengths = tuple([int(n) for n in lengths] + [1] * (3 - len(pairs)))
         self.halves = bool(halves)
-        self.table = torch.cat([rope_table(n, p, t).reshape(-1, 2) for n, p, t in
-                                zip(self.lengths, pairs, thetas) if p]).to(dev)
-        self._axes = torch.tensor(self.pairs + self.lengths, dtype=torch.int32)
+        self.table = torch.cat([rope_table(n, p, t, dev).reshape(-1, 2) for n, p, t in
+                                zip(self.lengths, pairs, thetas) if p])
+        self._axes = (ctypes.c_int32 * 6)(*self.pairs, *self.lengths)
         self.pos = self._positions(pos, dev)
 
     @staticmethod
@@ -439,8 +449,8 @@ def _token_rows(x: torch.Tensor, what: str):
     return [x.stride(i) if x.shape[i] > 1 else 0 for i in range(3)]
 
 
-def _strides6(a, b) -> torch.Tensor:
-    return torch.tensor(a + b, dtype=torch.int64)
+def _strides6(a, b):
+    return (ctypes.c_int64 * 6)(*a, *b)
 
 
 def _check_norm_rope(xq, xk, wq, wk, plan: RopePlan):
@@ -489,11 +499,11 @@ def qk_norm_rope(xq, xk, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor],
         q8, k8 = (Act8(torch.empty(B, N, h, D, device=dx.device, dtype=torch.int8),
                        torch.empty(B, N, h, device=dx.device, dtype=torch.float32)) for h in (Hq, Hk))
     if B * N > 0:
-        with torch.cuda.device(dx.device):
+        with _on(dx):
             st = lib().dsa_qk_norm_rope(
-                dx.data_ptr(), dk.data_ptr(), _ptr(sq), _ptr(sk), st6.data_ptr(), code, B, N, Hq, Hk, D,
+                dx.data_ptr(), dk.data_ptr(), _ptr(sq), _ptr(sk), st6, code, B, N, Hq, Hk, D,
                 _ptr(wq), _ptr(wk), float(eps), plan.table.data_ptr(), plan.pos.data_ptr(),
-                1 if plan.pos.shape[0] > 1 else 0, plan._axes.data_ptr(), int(plan.halves), q.data_ptr(),
+                1 if plan.pos.shape[0] > 1 else 0, plan._axes, int(plan.halves), q.data_ptr(),
                 k.data_ptr(), _ptr(q8.codes), _ptr(q8.scales), _ptr(k8.codes), _ptr(k8.scales),
                 _stream(dx))
         check(st, "dsa_qk_norm_rope")
@@ -535,12 +545,12 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, xq, xk, wq: Optional[to
     if workspace is None:
         workspace = torch.empty(int(lib().dsa_qk_norm_rope_bwd_workspace_size(D)), device=dq.device,
                                 dtype=torch.uint8)
-    with torch.cuda.device(dq.device):
+    with _on(dq):
         st = lib().dsa_qk_norm_rope_bwd(
-            dq.data_ptr(), dk.data_ptr(), vq.data_ptr(), vk.data_ptr(), _ptr(sq), _ptr(sk), st6.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), vq.data_ptr(), vk.data_ptr(), _ptr(sq), _ptr(sk), st6,
             code, B, N, Hq, Hk, D, _ptr(wq), _ptr(wk), float(eps), plan.table.data_ptr(),
-            plan.pos.data_ptr(), 1 if plan.pos.shape[0] > 1 else 0, plan._axes.data_ptr(),
-            int(plan.halves), dxq.data_ptr(), dxk.data_ptr(), dst6.data_ptr(), dwq.data_ptr(),
+            plan.pos.data_ptr(), 1 if plan.pos.shape[0] > 1 else 0, plan._axes,
+            int(plan.halves), dxq.data_ptr(), dxk.data_ptr(), dst6, dwq.data_ptr(),
             dwk.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
             _stream(dq))
     check(st, "dsa_qk_norm_rope_bwd")
@@ -587,7 +597,7 @@ def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int
         out = torch.empty_like(q)
     if want_lse and lse is None:
         lse = torch.empty(B, H, Nq, device=q.device, dtype=torch.float32)
-    with torch.cuda.device(q.device):
+    with _on(q):
         st = lib().dsa_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hk, Nq,
                                        Nk, D, scale, Nk - Nq if q_offset is None else int(q_offset),
                                        int(left), int(right), int(sink), out.data_ptr(), _ptr(lse), _stream(q))
@@ -606,15 +616,16 @@ def window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
         raise ValueError("the forward's lse is required")
     _check_lse(lse, q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    q_offset = Nk - Nq if q_offset is None else int(q_offset)
+    dt, left, right, sink = _dtype_code(q), int(left), int(right), int(sink)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
-        n = int(lib().dsa_window_attn_bwd_workspace_size(B, H, Nq))
+        n = int(lib().dsa_window_attn_bwd_workspace_size(dt, B, H, Hk, Nq, Nk, D, q_offset, left, right, sink))
         workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
-    with torch.cuda.device(q.device):
+    with _on(q):
         st = lib().dsa_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                       dout.data_ptr(), lse.data_ptr(), _dtype_code(q), B, H, Hk, Nq, Nk, D,
-                                       scale, Nk - Nq if q_offset is None else int(q_offset), int(left),
-                                       int(right), int(sink), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                       dout.data_ptr(), lse.data_ptr(), dt, B, H, Hk, Nq, Nk, D, scale,
+                                       q_offset, left, right, sink, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                        _stream(q))
     check(st, "dsa_window_attn_bwd")
@@ -651,8 +662,8 @@ def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if workspace is None:
         n = int(lib().dsa_window_attn_decode_workspace_size(dt, B, H, Hk, Nq, cap, D, int(left), int(sink)))
         workspace = torch.empty(n, device=q.device, dtype=torch.uint8) if n else None
-    with torch.cuda.device(q.device):
-        st = lib().dsa_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), st6.data_ptr(),
+    with _on(q):
+        st = lib().dsa_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), st6,
                                           dt, B, H, Hk, Nq, cap, D, scale, lens.data_ptr(), int(left),
                                           int(sink), out.data_ptr(), _ptr(lse), _ptr(workspace),
                                           0 if workspace is None else workspace.numel() * workspace.element_size(),

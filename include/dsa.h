@@ -438,17 +438,18 @@ dsa_status dsa_permute_tokens(const void* src, void* dst, dsa_dtype dt, int B, i
                               const int32_t* perm, int inverse, void* stream);
 
 /*
- * The (cos, sin) table of one rotation axis (host function, no device work):
+ * The (cos, sin) table of one rotation axis:
  *   table[(p * pairs + i) * 2 + {0, 1}] = cos, sin of p * theta^(-i / pairs)
  * for p = 0 .. positions-1, i = 0 .. pairs-1, computed in 64 bits (a position
  * of 100,000 turns its fastest pair 15,900 times; an fp32 angle would keep
  * two digits of the turn) and rounded to fp32.
  * The table of dsa_qk_norm_rope is the axes' tables one after another.
- *   table  host out, fp32 [positions][pairs][2].
- * Errors: DSA_ERR_INVALID_ARG for a null table, positions < 1, pairs outside
- * 1..64, theta not finite or <= 0, or positions * pairs above 2^30.
+ *   table  device out, fp32 [positions][pairs][2], 8-byte aligned.
+ * Errors: DSA_ERR_INVALID_ARG for a null or misaligned table, positions < 1,
+ * pairs outside 1..64, theta not finite or <= 0, or positions * pairs above
+ * 2^30.
  */
-dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table);
+dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table, void* stream);
 
 /*
  * Per-head norms of queries and keys with the position rotation, one pass
@@ -565,7 +566,7 @@ dsa_status dsa_window_attn_fwd(const void* q, const void* k, const void* v, dsa_
  *   out, lse   the forward's (lse is required);  dout  [B, H, Nq, D] in dt.
  *   dq         out, [B, H, Nq, D];  dk, dv  out, [B, Hk, Nk, D], in dt.  Keys
  *              that no query sees get 0, queries that see no key get dQ = 0.
- *   workspace  >= dsa_window_attn_bwd_workspace_size(B, H, Nq) bytes, 16-byte
+ *   workspace  >= dsa_window_attn_bwd_workspace_size(...) bytes, 16-byte
  *              aligned.
  * Every sum has a fixed order: two calls give the same bits.  bf16 runs on
  * tcgen05 with dS as two bf16 terms and P as one; fp32 in exact fp32.
@@ -577,8 +578,11 @@ dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, cons
                                int right, int sink, void* dq, void* dk, void* dv, void* workspace,
                                size_t ws_bytes, void* stream);
 
-/* Device workspace bytes for dsa_window_attn_bwd; 0 for invalid sizes. */
-size_t dsa_window_attn_bwd_workspace_size(int B, int H, int Nq);
+/* Device workspace bytes for dsa_window_attn_bwd with these arguments; 0 for
+ * invalid sizes.  (The row terms delta; in fp32 also the partial sums of
+ * gradient tiles that several CTAs share.) */
+size_t dsa_window_attn_bwd_workspace_size(dsa_dtype dt, int B, int H, int Hk, int Nq, int Nk, int D,
+                                          int q_offset, int left, int right, int sink);
 
 /*
  * The causal window attention (right = 0) of the newest Nq tokens of each
