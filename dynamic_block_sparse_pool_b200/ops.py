@@ -24,7 +24,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(t: torch.Tensor):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # the handle alone: a Stream object costs 2 us, as much as a launch
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _on(t: torch.Tensor):
@@ -328,8 +329,7 @@ def pack8(x: torch.Tensor) -> Act8:
     if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
         raise ValueError("x must be a contiguous CUDA tensor [..., D]")
     dt, D = _dtype_code(x), x.shape[-1]
-    a = Act8(torch.empty(x.shape, device=x.device, dtype=torch.int8),
-             torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32))
+    a = Act8(torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32))
     if x.numel() == 0:
         return a
     with _on(x):
@@ -344,7 +344,7 @@ def unpack8(a: Act8, dtype: torch.dtype = torch.bfloat16,
     """The values that 8-bit rows stand for, as bf16 or fp32."""
     _check_act8(a)
     if out is None:
-        out = torch.empty(a.codes.shape, device=a.codes.device, dtype=dtype)
+        out = torch.empty_like(a.codes, dtype=dtype)
     elif out.shape != a.codes.shape or out.device != a.codes.device or not out.is_contiguous():
         raise ValueError("out must be contiguous, of the codes' shape and device")
     dt, D = _dtype_code(out), out.shape[-1]
@@ -490,14 +490,14 @@ def qk_norm_rope(xq, xk, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor],
     if save8 and from8:
         raise ValueError("save8: xq and xk already are 8-bit rows")
     dt = dtype if from8 else dx.dtype
-    q = torch.empty(B, Hq, N, D, device=dx.device, dtype=dt)
-    k = torch.empty(B, Hk, N, D, device=dx.device, dtype=dt)
+    q = dx.new_empty((B, Hq, N, D), dtype=dt)
+    k = dx.new_empty((B, Hk, N, D), dtype=dt)
     code = _dtype_code(q)
     st6 = _strides6(_token_rows(dx, "xq"), _token_rows(dk, "xk"))
     q8 = k8 = Act8(None, None)
     if save8:
-        q8, k8 = (Act8(torch.empty(B, N, h, D, device=dx.device, dtype=torch.int8),
-                       torch.empty(B, N, h, device=dx.device, dtype=torch.float32)) for h in (Hq, Hk))
+        q8, k8 = (Act8(dx.new_empty((B, N, h, D), dtype=torch.int8),
+                       dx.new_empty((B, N, h), dtype=torch.float32)) for h in (Hq, Hk))
     if B * N > 0:
         with _on(dx):
             st = lib().dsa_qk_norm_rope(
@@ -529,7 +529,7 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, xq, xk, wq: Optional[to
     outs = []
     for d, h in ((dxq, Hq), (dxk, Hk)):
         if d is None:
-            d = torch.empty(B, N, h, D, device=dq.device, dtype=dq.dtype)
+            d = dq.new_empty((B, N, h, D))
         elif tuple(d.shape) != (B, N, h, D) or d.dtype != dq.dtype or d.device != dq.device:
             raise ValueError("dxq and dxk must be [B, N, H, D] of dq's dtype and device")
         elif any(d.shape[i] > 1 and d.stride(i) == 0 for i in range(3)):
@@ -538,13 +538,11 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, xq, xk, wq: Optional[to
     dxq, dxk = outs
     st6 = _strides6(_token_rows(vq, "xq"), _token_rows(vk, "xk"))
     dst6 = _strides6(_token_rows(dxq, "dxq"), _token_rows(dxk, "dxk"))
-    dwq = torch.empty(D, device=dq.device, dtype=torch.float32)
-    dwk = torch.empty(D, device=dq.device, dtype=torch.float32)
+    dwq, dwk = dq.new_empty(D, dtype=torch.float32), dq.new_empty(D, dtype=torch.float32)
     if B * N == 0:
         return dxq, dxk, dwq.zero_(), dwk.zero_()
     if workspace is None:
-        workspace = torch.empty(int(lib().dsa_qk_norm_rope_bwd_workspace_size(D)), device=dq.device,
-                                dtype=torch.uint8)
+        workspace = dq.new_empty(int(lib().dsa_qk_norm_rope_bwd_workspace_size(D)), dtype=torch.uint8)
     with _on(dq):
         st = lib().dsa_qk_norm_rope_bwd(
             dq.data_ptr(), dk.data_ptr(), vq.data_ptr(), vk.data_ptr(), _ptr(sq), _ptr(sk), st6,
@@ -596,7 +594,7 @@ def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int
     if out is None:
         out = torch.empty_like(q)
     if want_lse and lse is None:
-        lse = torch.empty(B, H, Nq, device=q.device, dtype=torch.float32)
+        lse = q.new_empty((B, H, Nq), dtype=torch.float32)
     with _on(q):
         st = lib().dsa_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hk, Nq,
                                        Nk, D, scale, Nk - Nq if q_offset is None else int(q_offset),
@@ -621,7 +619,7 @@ def window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
         n = int(lib().dsa_window_attn_bwd_workspace_size(dt, B, H, Hk, Nq, Nk, D, q_offset, left, right, sink))
-        workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+        workspace = q.new_empty(max(n, 16), dtype=torch.uint8)
     with _on(q):
         st = lib().dsa_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                        dout.data_ptr(), lse.data_ptr(), dt, B, H, Hk, Nq, Nk, D, scale,
@@ -661,7 +659,7 @@ def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     Hk, cap, dt = k_cache.shape[1], k_cache.shape[2], _dtype_code(q)
     if workspace is None:
         n = int(lib().dsa_window_attn_decode_workspace_size(dt, B, H, Hk, Nq, cap, D, int(left), int(sink)))
-        workspace = torch.empty(n, device=q.device, dtype=torch.uint8) if n else None
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
     with _on(q):
         st = lib().dsa_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), st6,
                                           dt, B, H, Hk, Nq, cap, D, scale, lens.data_ptr(), int(left),
