@@ -34,7 +34,7 @@ pack8_kernel(const T* __restrict__ x, long long rows, int8_t* __restrict__ codes
     Pair v[4];
     float scale;
     values(raw[u], v);
-    const uint2 c = encode8<TPR>(v, top_bits(raw[u]), scale);
+    const uint2 c = encode8(v, row_top<TPR>(top_bits(raw[u])), scale);
     const long long r = r0 + u * RPC;
     if (r < rows) {
       *reinterpret_cast<uint2*>(codes + r * D + 8 * sub) = c;

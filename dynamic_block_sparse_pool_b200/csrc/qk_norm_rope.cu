@@ -190,18 +190,18 @@ qk_norm_rope_kernel(const FwdArgs<TIn, TOut> a) {
       const int h = h0 + u * RPW;
       Pair v[4];
       values(raw[u], v);
+      Pair ss = 0ull;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) ss = fma_f32x2(v[m], v[m], ss);
       if constexpr (SAVE8) {
         float scale;
-        const uint2 c = encode8<TPR>(v, top_bits(raw[u]), scale);
+        const uint2 c = encode8(v, row_top<TPR>(top_bits(raw[u])), scale);
         if (h < heads) {
           const long long row = (long long)token * heads + h;
           *reinterpret_cast<uint2*>((is_k ? a.ck : a.cq) + row * D + 8 * sub) = c;
           if (sub == 0) (is_k ? a.sk : a.sq)[row] = scale;
         }
       }
-      Pair ss = 0ull;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) ss = fma_f32x2(v[m], v[m], ss);
       // (8-bit rows: v holds the codes, the row is scale * v)
       const float scale = scale_of(raw[u]);
       const Pair r = both(scale * rsqrtf(scale * scale * row_sum<TPR>(added(ss)) * (1.0f / D) + a.eps));
@@ -238,23 +238,27 @@ struct BwdArgs {
 };
 
 // A thread's eight values into its slots, and back.
-__device__ __forceinline__ void fetch_async(uint32_t slot, const __nv_bfloat16* p, const float*) { copy_async<16>(slot, p); }
-__device__ __forceinline__ void fetch_async(uint32_t slot, const float* p, const float*) {
+__device__ __forceinline__ void fetch_async(uint32_t slot, const __nv_bfloat16* p, const float*, int) {
+  copy_async<16>(slot, p);
+}
+__device__ __forceinline__ void fetch_async(uint32_t slot, const float* p, const float*, int) {
   copy_async<16>(slot, p);
   copy_async<16>(slot + 16 * kThreads, p + 4);
 }
-__device__ __forceinline__ void fetch_async(uint32_t slot, const int8_t* p, const float* scale) {
+// (the row's first thread brings in the scale for all of them)
+__device__ __forceinline__ void fetch_async(uint32_t slot, const int8_t* p, const float* scale, int sub) {
   copy_async<8>(slot, p);
-  copy_async<4>(slot + 8, scale);
+  if (sub == 0) copy_async<4>(slot + 8, scale);
 }
-__device__ __forceinline__ void read_slot(const uint4* slot, Raw<__nv_bfloat16>& r) { r.v = slot[0]; }
-__device__ __forceinline__ void read_slot(const uint4* slot, Raw<float>& r) {
+__device__ __forceinline__ void read_slot(const uint4* slot, Raw<__nv_bfloat16>& r, int) { r.v = slot[0]; }
+__device__ __forceinline__ void read_slot(const uint4* slot, Raw<float>& r, int) {
   r.v = slot[0];
   r.w = slot[kThreads];
 }
-__device__ __forceinline__ void read_slot(const uint4* slot, Raw<int8_t>& r) {
-  r.v = make_uint2(slot->x, slot->y);
-  r.scale = __uint_as_float(slot->z);
+__device__ __forceinline__ void read_slot(const uint4* slot, Raw<int8_t>& r, int sub) {
+  __syncwarp();  // the scale is another thread's copy, and that thread has waited for it
+  r.v = *reinterpret_cast<const uint2*>(slot);
+  r.scale = *reinterpret_cast<const float*>(reinterpret_cast<const uint32_t*>(slot - sub) + 2);
 }
 
 // Steps of the backward whose loads are in flight: enough bytes for HBM's
@@ -306,8 +310,8 @@ qk_norm_rope_bwd_kernel(const BwdArgs<TX, TG> a) {
     if (ft < tokens) {
       if (fh < hz) {  // (a lane past the heads leaves its slots as they are)
         const uint32_t to = ring0 + (fs % kDepth) * (SLOTS * kThreads * 16);
-        fetch_async(to, px, ps);
-        fetch_async(to + SX * kThreads * 16, pg, nullptr);
+        fetch_async(to, px, ps, sub);
+        fetch_async(to + SX * kThreads * 16, pg, nullptr, sub);
       }
       ++fs;
       fh += RPW;
@@ -337,8 +341,8 @@ qk_norm_rope_bwd_kernel(const BwdArgs<TX, TG> a) {
       ++rs;
       Raw<TX> raw;
       Raw<TG> grad;
-      read_slot(from, raw);
-      read_slot(from + SX * kThreads, grad);
+      read_slot(from, raw, sub);
+      read_slot(from + SX * kThreads, grad, sub);
       const bool in = h < hz;
       Pair x[4], g[4], ss = 0ull, dot = 0ull;
       values(raw, x);

@@ -147,11 +147,17 @@ __device__ __forceinline__ uint32_t top_bits(const Raw<float>& r) {
              max(max(r.w.x & kMag, r.w.y & kMag), max(r.w.z & kMag, r.w.w & kMag)));
 }
 
-// The row's codes and scale from its threads' values (see above).
+// Over the row's threads.
 template <int TPR>
-__device__ __forceinline__ uint2 encode8(const Pair (&x)[4], uint32_t top, float& scale) {
+__device__ __forceinline__ uint32_t row_top(uint32_t top) {
 #pragma unroll
   for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top;
+}
+
+// A thread's codes and the row's scale, from the row's largest magnitude (see
+// above).
+__device__ __forceinline__ uint2 encode8(const Pair (&x)[4], uint32_t top, float& scale) {
   const float amax = __uint_as_float(top);
   float inv = 0.f;
   scale = 0.f;
