@@ -146,7 +146,9 @@ dsa_status window_args(dsa::WindowAttn& a, const void* q, const void* k, const v
 size_t delta_bytes(const dsa::WindowAttn& a) { return ((size_t)a.B * a.H * a.w.Nq * sizeof(float) + 15) / 16 * 16; }
 
 size_t window_bwd_bytes(const dsa::WindowAttn& a, dsa_dtype dt) {
-  return delta_bytes(a) + (dt == DSA_F32 ? dsa::simt_share_floats(a.B, a.H, a.Hk, a.w, a.D) * sizeof(float) : 0);
+  if (dt == DSA_F32) return delta_bytes(a) + dsa::simt_share_floats(a.B, a.H, a.Hk, a.w, a.D) * sizeof(float);
+  const size_t slots = dsa::bwd_chunks(a.B, a.H, a.Hk, a.w).slots((a.w.Nk + 127) / 128);
+  return delta_bytes(a) + slots * 2 * 128 * a.D * sizeof(float);
 }
 
 }  // namespace

@@ -65,6 +65,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// Waits for a phase of each of two barriers, polling both at once.
+__device__ __forceinline__ bool mbar_wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+  bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
+  if (a && b) return true;
+  const unsigned long long t0 = global_timer_ns();
+  while (true) {
+    if (!a) a = mbar_try_wait(bar0, parity0);
+    if (!b) b = mbar_try_wait(bar1, parity1);
+    if (a && b) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
 // mbar_wait for a warp that has nothing else to do while it waits (the MMA
 // issuer, the TMA loader): between polls it sleeps for about sleep_ns, so
 // its polling does not compete with the softmax warps of its SM

@@ -5,6 +5,44 @@
 
 namespace dsa {
 
+// How the pairs of a key tile (128 keys) are cut among CTAs in the bf16 dK/dV
+// kernel: tiles with sinks (kind 0) and the others (kind 1) alike among
+// themselves.
+struct BwdChunks {
+  int heads, sink_tiles;
+  int chunks[2], counts[2];  // pairs of a part, parts of a tile
+  __host__ __device__ bool kind(int tile) const { return tile >= sink_tiles; }
+  __host__ __device__ int chunk(int tile) const { return kind(tile) ? chunks[1] : chunks[0]; }
+  __host__ __device__ int parts(int tile) const { return kind(tile) ? counts[1] : counts[0]; }
+  // CTAs of a head, and what CTA i of them does
+  __host__ __device__ int ctas(int tiles) const {
+    return sink_tiles * counts[0] + (tiles - sink_tiles) * counts[1];
+  }
+  __host__ __device__ void place(int i, int& tile, int& part) const {
+    const int first = sink_tiles * counts[0], n = i >= first ? counts[1] : counts[0];
+    const int t = i >= first ? sink_tiles : 0;
+    if (i >= first) i -= first;
+    tile = t + i / n;
+    part = i % n;
+  }
+  // tiles of a head that are cut, and the i-th of them
+  __host__ __device__ int cut_tiles(int tiles) const {
+    return (counts[0] > 1 ? sink_tiles : 0) + (counts[1] > 1 ? tiles - sink_tiles : 0);
+  }
+  __host__ __device__ int cut_tile(int i) const { return counts[0] > 1 ? i : sink_tiles + i; }
+  // place of a part's share: the cut kinds one after the other
+  __host__ __device__ size_t slot(int head, int tiles, int tile, int part) const {
+    const size_t first = counts[0] > 1 ? (size_t)heads * sink_tiles * counts[0] : 0;
+    if (tile < sink_tiles) return ((size_t)head * sink_tiles + tile) * counts[0] + part;
+    return first + ((size_t)head * (tiles - sink_tiles) + tile - sink_tiles) * counts[1] + part;
+  }
+  __host__ __device__ size_t slots(int tiles) const {
+    return (size_t)heads * ((counts[0] > 1 ? (size_t)sink_tiles * counts[0] : 0) +
+                            (counts[1] > 1 ? (size_t)(tiles - sink_tiles) * counts[1] : 0));
+  }
+};
+BwdChunks bwd_chunks(int B, int H, int Hk, const Window& w);
+
 struct WindowAttn {
   int B, H, Hk, D;
   Window w;
@@ -16,7 +54,7 @@ struct WindowAttn {
   const void *o, *dout;       // the forward's output and its gradient
   void *dq, *dk, *dv;
   float* delta;               // workspace, [B, H, Nq]
-  float* shares;              // workspace, simt_share_floats (fp32)
+  float* shares;              // workspace: sums of gradient tiles that several CTAs share
   int num_sms;
   unsigned* err;
 };

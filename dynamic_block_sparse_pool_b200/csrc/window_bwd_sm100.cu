@@ -9,6 +9,8 @@
 //   dq    one query tile against the key tiles it sees;
 //   dkdv  one key tile against the query tiles that see it, for each query
 //         head of its group in turn: every sum has a fixed order, no atomics.
+//         A tile that many more queries see than the others (one with sinks) is
+//         cut into several CTAs, whose fp32 shares window_join adds in order.
 // Per tile pair the S-type products go to tensor memory as fp32, the
 // element-wise pass writes packed bf16 terms back into S's columns, and the
 // gradient products take them from there.  For dQ, dS goes in as two terms,
@@ -18,13 +20,31 @@
 // over queries, whose terms have no such bond: P and dS go in as one term each
 // (half a step, at most 2^-8 of each, as P in the forward).
 //
-// Each tile pair runs as two halves of 64 columns: warps 0-3 own half 0 and
-// warps 4-7 half 1 (one row per thread), each half with its own barriers, so
-// while one half is in its element-wise pass the tensor cores work for the
-// other.  Warp 8 issues the MMAs, warp 9 the TMA loads into a ring of two
-// stages (three at D = 64).  Tensor memory: S 0-127, dP 128-255, gradients from
-// 256.  Every mbarrier wait is bounded; a timeout sets the device error word
-// and the CTA winds down.
+// The element-wise pass (eight warps: one row per thread, warps 0-3 the first 64
+// columns, warps 4-7 the others) is what bounds the kernels, so everything else
+// goes on beside it.
+//   dQ: S has two buffers in tensor memory.  While pair e is in its element-wise
+//   pass, S of e + 1 is done already and dP of e + 1 runs as soon as dP of e has
+//   been read; the gradient products of e run, half by half, under the pass of
+//   e + 1, and S of e + 2 follows them into the buffer of e (the MMAs of one
+//   thread run in order).
+//   dK, dV: one buffer; each half's S of e + 1 follows the half's gradient
+//   products of e, so one half's pass goes on while the other half waits.  At
+//   D = 64 dP of e + 1 is done before them, as in dQ; at D = 128, where shared
+//   memory holds two stages of each ring and not three, it follows S.
+// Measured, 17,776 tokens, 8 heads, D = 64, every token in sight of 5,400 others
+// and a prefix of 226: dQ 458 us with two buffers of S, 511 with one; dK/dV 624
+// with one, 644 with two.  8,192 tokens, 16 query heads on 4, D = 128, causal
+// over 2,048: dQ 243 (256 with one), dK/dV 357 with S and dP behind the
+// gradients, 376 with dP ahead of them.
+// Warp 8 issues the MMAs, warp 9 the TMA loads into two rings, one for each
+// streamed tensor.  Every mbarrier wait is bounded; a timeout sets the device
+// error word and the CTA winds down.
+// All three kernels with the row terms: 5.2 ms for 17,776 tokens, 48 heads,
+// D = 64, the mask above (545 TFLOP/s); 0.63 ms for the D = 128 shape above with
+// four sinks (475).
+#include <algorithm>
+
 #include "bwd_tiles.cuh"
 #include "tile_map.cuh"
 #include "window_attn.cuh"
@@ -34,32 +54,51 @@ namespace {
 
 using namespace bwd;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
+// warps 10 and 11 only fill up the third warpgroup: of its registers (168 a thread
+// at launch) the element-wise warps take what it does not need
+// (5.29 -> 5.19 ms at D = 64, 0.62 -> 0.63 at D = 128, the shapes above)
+constexpr int kElementRegs = 208, kOtherRegs = 88;
+static_assert(256 * kElementRegs + 128 * kOtherRegs <= 168 * kThreads);
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColP = 128, kColG = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Barriers, with room for three ring stages; kBarR: a half's dP is read out of
-// tensor memory (D = 64), kBarP: its terms are written.
-enum : int { kBarFixed = 0, kBarRing = 1, kBarFree = 4, kBarS = 7, kBarP = 9, kBarR = 11, kBarDrain = 13,
-             kNumBars = 14 };
+// Barriers, with room for three stages of each ring.  kBarS (+ half, with one
+// buffer of S): S and dP of a pair are done; kBarR: dP is read out of tensor
+// memory (eight warps; where dP of the next pair comes early); kBarP + 2 (pair % 2) + half: the half's terms are written
+// (four warps).  With two buffers of S a warp may be done with pair e + 1 before
+// another one is with e, so their arrivals must not meet on one barrier; e + 2 it
+// cannot reach, since S and dP of it wait for every warp's kBarR of e + 1.
+enum : int { kBarFixed = 0, kBarRingA = 1, kBarRingB = 4, kBarFreeA = 7, kBarFreeB = 10, kBarS = 13, kBarR = 15,
+             kBarP = 16, kBarDrain = 20, kNumBars = 21 };
 
-template <int D>
-struct Smem {
+// Tensor and shared memory of a kernel with NG gradient accumulators.  The
+// streamed tile A is read by S and by a gradient product, two pairs apart where
+// S has two buffers; B by dP and, with NG = 2, by a gradient product.  A tile
+// that is needed before the gradient products of the pair before has a third
+// stage, so that its load does not wait for them.
+template <int D, int NG>
+struct Layout {
+  static constexpr bool kTwoS = NG == 1;
+  static constexpr bool kEarlyP = NG == 1 || D == 64;  // dP of the next pair before the gradient products
+  static constexpr uint32_t kColP = kTwoS ? 2 * BB : BB, kColG = kColP + BB;  // dP, gradients (S at 0)
   static constexpr int kTile = BB * D * 2;
-  static constexpr int kStages = D == 64 ? 3 : 2;       // of the streamed tiles
-  static constexpr int kFixA = 0, kFixB = kTile;        // the CTA's own two tiles
+  static constexpr int kStagesA = kEarlyP ? 3 : 2, kStagesB = kEarlyP && NG == 2 ? 3 : 2;
+  static constexpr int kFixA = 0, kFixB = kTile;          // the CTA's own two tiles
   static constexpr int kRingA = 2 * kTile;
-  static constexpr int kRingB = kRingA + kStages * kTile;
-  static constexpr int kVec = kRingB + kStages * kTile;  // float [2][-lse2 | -delta][128] (dkdv)
-  static constexpr int kBar = kVec + 2 * 2 * BB * 4;
+  static constexpr int kRingB = kRingA + kStagesA * kTile;
+  static constexpr int kVec = kRingB + kStagesB * kTile;  // float [2][-lse2 | -delta][128] (dkdv)
+  static constexpr int kBar = kVec + (NG == 2 ? 2 * 2 * BB * 4 : 0);
   static constexpr int kSlot = kBar + 8 * kNumBars;
   static constexpr int kBytes = kSlot + 16;
+  static __device__ __forceinline__ uint32_t s_col(int it) { return kTwoS ? (uint32_t)(BB * (it & 1)) : 0u; }
 };
 
 struct BwdParams {
   Window w;
+  BwdChunks cut;   // dkdv
+  float* shares;   // dkdv: [slot][dV, dK][128][D]
   int group;       // query heads per key head
   int tiles;       // tiles per head of the CTA's side
   float scale, scale_log2;
@@ -78,9 +117,8 @@ struct Cta {
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
 };
 
-template <int D>
+template <typename L>
 __device__ __forceinline__ bool cta_begin(Cta& c, uint8_t* smem, unsigned* err) {
-  using L = Smem<D>;
   c.smem = smem;
   c.base = smem_u32(smem);
   c.warp = threadIdx.x >> 5;
@@ -94,8 +132,7 @@ __device__ __forceinline__ bool cta_begin(Cta& c, uint8_t* smem, unsigned* err) 
   c.abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
   if (c.warp == kMmaWarp) {
     if (c.lane == 0) {
-      // a half's four warps arrive on kBarP and kBarR
-      for (int i = 0; i < kNumBars; ++i) mbar_init(c.bar(i), i >= kBarP && i < kBarR + 2 ? 4u : 1u);
+      for (int i = 0; i < kNumBars; ++i) mbar_init(c.bar(i), i == kBarR ? 8u : i >= kBarP && i < kBarP + 4 ? 4u : 1u);
       *c.abort_flag = 0;
       fence_mbar_init();
     }
@@ -112,9 +149,8 @@ __device__ __forceinline__ bool cta_begin(Cta& c, uint8_t* smem, unsigned* err) 
 
 // After a role gave up, copies and MMAs may still be in flight: they finish
 // (bounded) before shared and tensor memory are released.
-template <int D>
-__device__ __forceinline__ void cta_end(const Cta& c, int n, int issued) {
-  constexpr int ST = Smem<D>::kStages;
+template <typename L>
+__device__ __forceinline__ void cta_end(const Cta& c, int n, int issued_a, int issued_b) {
   tc_fence_before();
   __syncthreads();
   if (*c.abort_flag) {
@@ -125,8 +161,10 @@ __device__ __forceinline__ void cta_end(const Cta& c, int n, int issued) {
       }
       __syncwarp();
     } else if (c.warp == kLoadWarp && c.lane == 0 && n > 0) {
-      for (int b = issued > ST ? issued - ST : 0; b < issued; ++b)
-        mbar_wait(c.bar(kBarRing + b % ST), (uint32_t)(b / ST) & 1u);
+      for (int b = max(0, issued_a - L::kStagesA); b < issued_a; ++b)
+        mbar_wait(c.bar(kBarRingA + b % L::kStagesA), (uint32_t)(b / L::kStagesA) & 1u);
+      for (int b = max(0, issued_b - L::kStagesB); b < issued_b; ++b)
+        mbar_wait(c.bar(kBarRingB + b % L::kStagesB), (uint32_t)(b / L::kStagesB) & 1u);
       mbar_wait(c.bar(kBarFixed), 0u);
     }
     tc_fence_before();
@@ -143,124 +181,137 @@ __device__ __forceinline__ void give_up(const Cta& c, unsigned* err) {
   if (c.lane == 0) flag_error(err, kErrTimeout);
 }
 
-// S and dP of a half are in registers (the waits); with `tell`, the MMA issuer
-// learns that dP's columns are free.
-__device__ __forceinline__ void read_out(const Cta& c, int h, uint32_t (&sv)[2][32], uint32_t (&pv)[2][32], bool tell) {
+// S and dP of half h in registers; then dP's columns are free.
+template <typename L>
+__device__ __forceinline__ void read_half(const Cta& c, uint32_t lanes, uint32_t s_col, int h, uint32_t (&sv)[2][32],
+                                          uint32_t (&pv)[2][32]) {
+#pragma unroll
+  for (int cc = 0; cc < 2; ++cc) {
+    tmem_ld32(c.tmem + lanes + s_col + 64 * h + 32 * cc, sv[cc]);
+    tmem_ld32(c.tmem + lanes + L::kColP + 64 * h + 32 * cc, pv[cc]);
+  }
 #pragma unroll
   for (int cc = 0; cc < 2; ++cc) {
     tmem_wait_ld_regs(sv[cc]);
     tmem_wait_ld_regs(pv[cc]);
   }
-  if (tell) {
+  if (L::kEarlyP) {
     tc_fence_before();
     __syncwarp();
-    if (c.lane == 0) mbar_arrive(c.bar(kBarR + h));
+    if (c.lane == 0) mbar_arrive(c.bar(kBarR));
   }
 }
 
-// The loader's part: the fixed tiles of row f0 of head fh, then for it < n
-// the two streamed tiles of head(it), row(it).
-template <int D, typename Where>
-__device__ __forceinline__ int load_tiles(const Cta& c, const CUtensorMap* fa, const CUtensorMap* fb, int f0, int fh,
-                                          const CUtensorMap* sa, const CUtensorMap* sb, int n, Where where,
-                                          unsigned* err) {
-  using L = Smem<D>;
+// The loader's part: the fixed tiles of row f0 of head fh, then for it < n the
+// two streamed tiles of head(it), row(it).
+template <int D, typename L, typename Where>
+__device__ __forceinline__ void load_tiles(const Cta& c, const CUtensorMap* fa, const CUtensorMap* fb, int f0, int fh,
+                                           const CUtensorMap* sa, const CUtensorMap* sb, int n, Where where,
+                                           int& issued_a, int& issued_b, unsigned* err) {
   constexpr uint32_t kTileBytes = L::kTile;
-  int issued = 0;
   mbar_expect_tx(c.bar(kBarFixed), 2 * kTileBytes);
   tma_tile<D>(c.base + L::kFixA, fa, f0, fh, c.bar(kBarFixed));
   tma_tile<D>(c.base + L::kFixB, fb, f0, fh, c.bar(kBarFixed));
   for (int it = 0; it < n; ++it) {
-    const int s = it % L::kStages;
+    const int a = it % L::kStagesA, b = it % L::kStagesB;
     int head, row;
     where(it, head, row);
-    if (!mbar_wait(c.bar(kBarFree + s), ((uint32_t)(it / L::kStages) & 1u) ^ 1u) || *c.abort_flag) {
+    if (!mbar_wait(c.bar(kBarFreeA + a), ((uint32_t)(it / L::kStagesA) & 1u) ^ 1u) || *c.abort_flag) {
       give_up(c, err);
-      break;
+      return;
     }
-    mbar_expect_tx(c.bar(kBarRing + s), 2 * kTileBytes);
-    tma_tile<D>(c.base + L::kRingA + s * kTileBytes, sa, row, head, c.bar(kBarRing + s));
-    tma_tile<D>(c.base + L::kRingB + s * kTileBytes, sb, row, head, c.bar(kBarRing + s));
-    issued = it + 1;
+    mbar_expect_tx(c.bar(kBarRingA + a), kTileBytes);
+    tma_tile<D>(c.base + L::kRingA + a * kTileBytes, sa, row, head, c.bar(kBarRingA + a));
+    ++issued_a;
+    if (!mbar_wait(c.bar(kBarFreeB + b), ((uint32_t)(it / L::kStagesB) & 1u) ^ 1u) || *c.abort_flag) {
+      give_up(c, err);
+      return;
+    }
+    mbar_expect_tx(c.bar(kBarRingB + b), kTileBytes);
+    tma_tile<D>(c.base + L::kRingB + b * kTileBytes, sb, row, head, c.bar(kBarRingB + b));
+    ++issued_b;
   }
-  return issued;
 }
 
-// The MMA issuer's part: S = A a^T and dP = B b^T (A, B fixed, a, b streamed)
-// in halves of 64 streamed rows; `grads(half, stage, accumulate)` once a half's
-// terms are written.  The terms lie in S's columns, so the next pair's S
-// follows the gradient products (the MMAs of one thread run in order).  dP's
-// columns are free as soon as they are read: with three ring stages (D = 64)
-// the next pair's dP runs while the half is in its element-wise pass (kEarly);
-// with two its tiles would not have landed.
-template <int D, typename Grads>
+// The MMA issuer's part: S = A a^T and dP = B b^T (A, B fixed, a, b streamed),
+// and `grads(half, column of S, stage of a, stage of b, accumulate)` once a
+// half's terms are written.
+template <int D, int NG, typename Grads>
 __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, unsigned* err) {
-  using L = Smem<D>;
-  constexpr uint32_t kTileBytes = L::kTile;
-  constexpr bool kEarly = L::kStages == 3;
+  using L = Layout<D, NG>;
+  constexpr uint32_t kTileBytes = L::kTile, kIdesc = idesc_bf16_f32(BB, BB, false);
   const uint32_t base = __shfl_sync(0xffffffffu, c.base, 0), tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
   const uint64_t dA = smem_desc_sw128(base + L::kFixA, 16, 1024), dB = smem_desc_sw128(base + L::kFixB, 16, 1024);
   const uint64_t da = smem_desc_sw128(base + L::kRingA, 16, 1024), db = smem_desc_sw128(base + L::kRingB, 16, 1024);
-  int st = 0, st1 = 0;    // ring stages of this pair and of the next
-  uint32_t ring_ph = 0;   // phase of the next pair's stage
-  bool ok = warp_all(mbar_wait(c.bar(kBarFixed), 0u)) && warp_all(mbar_wait(c.bar(kBarRing), 0u));
-  auto scores = [&](int stage, int h) {
-    mma_rows_half<D>(tmem + kColS + 64 * h, dA, da + (uint64_t)(stage * (kTileBytes >> 4)), h);
+  auto landed = [&](int ring, int it, int stages) {
+    return warp_all(mbar_wait(c.bar(ring + it % stages), (uint32_t)(it / stages) & 1u));
   };
-  auto dprobs = [&](int stage, int h) {
-    mma_rows_half<D>(tmem + kColP + 64 * h, dB, db + (uint64_t)(stage * (kTileBytes >> 4)), h);
-  };
-  if (ok) {
+  auto product = [&](uint32_t d, uint64_t x, uint64_t y) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (elect_one()) {
-        scores(0, h);
-        dprobs(0, h);
-        mma_commit(c.bar(kBarS + h));
-      }
+    for (int kk = 0; kk < D / 16; ++kk) mma_ss(d, x + kstep<D>(kk), y + kstep<D>(kk), kIdesc, kk > 0 ? 1u : 0u);
+  };
+  auto stage_a = [&](int it) { return (uint64_t)((it % L::kStagesA) * (kTileBytes >> 4)); };
+  auto scores = [&](int it) { product(tmem + L::s_col(it), dA, da + stage_a(it)); };
+  auto stage_b = [&](int it) { return (uint64_t)((it % L::kStagesB) * (kTileBytes >> 4)); };
+  auto dprobs = [&](int it) { product(tmem + L::kColP, dB, db + stage_b(it)); };
+  bool ok = warp_all(mbar_wait(c.bar(kBarFixed), 0u)) && landed(kBarRingA, 0, L::kStagesA) &&
+            landed(kBarRingB, 0, L::kStagesB);
+  if (ok) {
+    if (elect_one()) {
+      scores(0);
+      dprobs(0);
+      mma_commit(c.bar(kBarS));
+      if (!L::kTwoS) mma_commit(c.bar(kBarS + 1));
+      if (NG == 1) mma_commit(c.bar(kBarFreeB));
+    }
+    __syncwarp();
+    if (L::kTwoS && n > 1 && (ok = landed(kBarRingA, 1, L::kStagesA))) {
+      if (elect_one()) scores(1);
       __syncwarp();
     }
   }
   for (int it = 0; it < n && ok; ++it) {
     const bool more = it + 1 < n;
-    const uint32_t ph = (uint32_t)it & 1u;
-    st1 = st + 1;
-    if (st1 == L::kStages) {
-      st1 = 0;
-      ring_ph ^= 1u;
-    }
-    if (kEarly && more) {
-      if (!(ok = warp_all(mbar_wait(c.bar(kBarRing + st1), ring_ph)))) break;
-      if (!(ok = warp_all(mbar_wait(c.bar(kBarR), ph)) && warp_all(mbar_wait(c.bar(kBarR + 1), ph)))) break;
+    if (L::kEarlyP && more) {
+      if (!(ok = warp_all(mbar_wait_both(c.bar(kBarRingB + (it + 1) % L::kStagesB),
+                                         (uint32_t)((it + 1) / L::kStagesB) & 1u, c.bar(kBarR), (uint32_t)it & 1u))))
+        break;
       tc_fence_after();
-      if (elect_one()) {  // both halves at once: half as many MMAs
-        const uint64_t b0 = db + (uint64_t)(st1 * (kTileBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + kColP, dB + kstep<D>(kk), b0 + kstep<D>(kk), idesc_bf16_f32(BB, BB, false), kk > 0 ? 1u : 0u);
+      if (elect_one()) {
+        dprobs(it + 1);
+        if (L::kTwoS) mma_commit(c.bar(kBarS));
+        if (NG == 1) mma_commit(c.bar(kBarFreeB + (it + 1) % L::kStagesB));
       }
       __syncwarp();
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!(ok = ok && warp_all(mbar_wait(c.bar(kBarP + h), ph)))) break;
+      if (!(ok = ok && warp_all(mbar_wait(c.bar(kBarP + 2 * (it & 1) + h), (uint32_t)(it >> 1) & 1u)))) break;
       tc_fence_after();
       if (elect_one()) {
-        grads(h, (uint64_t)(st * (kTileBytes >> 4)), it > 0 || h > 0);
-        if (h == 1) mma_commit(c.bar(kBarFree + st));
+        grads(h, L::s_col(it), stage_a(it), stage_b(it), it > 0 || h > 0);
+        if (h == 1) mma_commit(c.bar(kBarFreeA + it % L::kStagesA));
+        if (h == 1 && NG == 2) mma_commit(c.bar(kBarFreeB + it % L::kStagesB));
       }
       __syncwarp();
-      if (more) {
-        if (!kEarly && h == 0 && !(ok = warp_all(mbar_wait(c.bar(kBarRing + st1), ring_ph)))) break;
+      if (!L::kTwoS && more) {  // the half's S follows at once
+        if (h == 0 && !(ok = landed(kBarRingA, it + 1, L::kStagesA) &&
+                             (L::kEarlyP || landed(kBarRingB, it + 1, L::kStagesB))))
+          break;
         if (elect_one()) {
-          scores(st1, h);
-          if (!kEarly) dprobs(st1, h);
+          mma_rows_half<D>(tmem + 64 * h, dA, da + stage_a(it + 1), h);
+          if (!L::kEarlyP) mma_rows_half<D>(tmem + L::kColP + 64 * h, dB, db + stage_b(it + 1), h);
           mma_commit(c.bar(kBarS + h));
         }
         __syncwarp();
       }
     }
-    st = st1;
+    if (!ok) break;
+    if (L::kTwoS && it + 2 < n) {
+      if (!(ok = landed(kBarRingA, it + 2, L::kStagesA))) break;
+      if (elect_one()) scores(it + 2);
+      __syncwarp();
+    }
   }
   if (!ok) give_up(c, err);
 }
@@ -270,31 +321,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const BwdParams p,
                  __nv_bfloat16* __restrict__ dq, unsigned* err) {
-  using L = Smem<D>;
+  using L = Layout<D, 1>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Cta c;
-  if (!cta_begin<D>(c, smem, err)) return;
+  if (!cta_begin<L>(c, smem, err)) return;
   const int bh = blockIdx.x / p.tiles, q0 = (blockIdx.x - bh * p.tiles) * BB;
   const int q1 = min(q0 + BB, p.w.Nq);
   const KeyTiles<BB> kt = KeyTiles<BB>::of(p.w, q0, q1);
   const int n = kt.count();
-  int issued = 0;
+  int issued_a = 0, issued_b = 0;
 
-  if (c.warp == kLoadWarp) {
-    if (c.lane == 0 && n > 0)
-      issued = load_tiles<D>(c, &tmQ, &tmO, q0, bh, &tmK, &tmV, n, [&](int it, int& head, int& row) {
-        head = bh / p.group;
-        row = kt.tile(it) * BB;
-      }, err);
-  } else if (c.warp == kMmaWarp) {
-    if (n > 0) {
-      const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
-      const uint64_t dKm = smem_desc_sw128(__shfl_sync(0xffffffffu, c.base, 0) + L::kRingA, kSubBytes, 1024);
-      issue_mmas<D>(c, n, [&](int h, uint64_t off, bool accumulate) {
-        mma_grad_half<D>(tmem + kColG, tmem + kColS, dKm + off, h, accumulate);  // dQ += dS K
-      }, err);
+  if (c.warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (c.warp == kLoadWarp) {
+      if (c.lane == 0 && n > 0)
+        load_tiles<D, L>(c, &tmQ, &tmO, q0, bh, &tmK, &tmV, n, [&](int it, int& head, int& row) {
+          head = bh / p.group;
+          row = kt.tile(it) * BB;
+        }, issued_a, issued_b, err);
+    } else if (c.warp == kMmaWarp) {
+      if (n > 0) {
+        const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
+        const uint64_t dKm = smem_desc_sw128(__shfl_sync(0xffffffffu, c.base, 0) + L::kRingA, kSubBytes, 1024);
+        issue_mmas<D, 1>(c, n, [&](int h, uint32_t s_col, uint64_t a, uint64_t, bool accumulate) {
+          mma_grad_half<D>(tmem + L::kColG, tmem + s_col, dKm + a, h, accumulate);  // dQ += dS K
+        }, err);
+      }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElementRegs));
     const int h = c.warp >> 2, row = 32 * (c.warp & 3) + c.lane;
     const uint32_t lanes = (uint32_t)(32 * (c.warp & 3)) << 16;
     const bool valid = q0 + row < q1;
@@ -309,15 +364,11 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int it = 0; it < n; ++it) {
       const int k0 = kt.tile(it) * BB;
       const bool whole = all_visible(p.w, q0, q1, k0, k0 + BB);
-      if (!(ok = warp_all(mbar_wait(c.bar(kBarS + h), (uint32_t)it & 1u)))) break;
+      if (!(ok = warp_all(mbar_wait(c.bar(kBarS + (L::kTwoS ? 0 : h)), (uint32_t)it & 1u)))) break;
       tc_fence_after();
+      const uint32_t s_col = L::s_col(it);
       uint32_t sv[2][32], pv[2][32];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        tmem_ld32(c.tmem + lanes + kColS + 64 * h + 32 * cc, sv[cc]);
-        tmem_ld32(c.tmem + lanes + kColP + 64 * h + 32 * cc, pv[cc]);
-      }
-      read_out(c, h, sv, pv, D == 64);
+      read_half<L>(c, lanes, s_col, h, sv, pv);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const uint32_t col = 64u * h + 32u * cc;
@@ -342,15 +393,15 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           unpack_f32x2(mul_f32x2(p2, d2), g0, g1);
           split_pair(g0, g1, dh[m], dl[m]);
         }
-        tmem_st16(c.tmem + lanes + kColS + col, dh);
-        tmem_st16(c.tmem + lanes + kColS + col + 16, dl);
+        tmem_st16(c.tmem + lanes + s_col + col, dh);
+        tmem_st16(c.tmem + lanes + s_col + col + 16, dl);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive(c.bar(kBarP + h));
+      if (c.lane == 0) mbar_arrive(c.bar(kBarP + 2 * (it & 1) + h));
     }
-    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFree + (n - 1) % L::kStages), (uint32_t)((n - 1) / L::kStages) & 1u));
+    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFreeA + (n - 1) % L::kStagesA), (uint32_t)((n - 1) / L::kStagesA) & 1u));
     if (!ok) {
       give_up(c, err);
     } else {
@@ -361,7 +412,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int col = h * (D / 2) + 32 * g32;
         uint32_t g[32];
         if (n > 0) {
-          tmem_ld32(c.tmem + lanes + kColG + col, g);
+          tmem_ld32(c.tmem + lanes + L::kColG + col, g);
           tmem_wait_ld_regs(g);
         } else {
 #pragma unroll
@@ -371,7 +422,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     }
   }
-  cta_end<D>(c, n, issued);
+  cta_end<L>(c, n, issued_a, issued_b);
 }
 
 template <int D>
@@ -379,36 +430,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const BwdParams p,
                    __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, unsigned* err) {
-  using L = Smem<D>;
-  constexpr uint32_t kColV = kColG, kColK = kColG + D;
+  using L = Layout<D, 2>;
+  constexpr uint32_t kColV = L::kColG, kColK = L::kColG + D;
+  const int ctas = p.cut.ctas(p.tiles), kv = blockIdx.x / ctas;
+  int tile, part;
+  p.cut.place(blockIdx.x - kv * ctas, tile, part);
+  const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
+  const QueryRun run = QueryRun::of(p.w, k0, k1);
+  const int i0 = run.q0 / BB, per = run.tiles<BB>();
+  // pairs e0 .. e0 + n - 1 of the tile: query tiles per head, head after head
+  const int e0 = part * p.cut.chunk(tile), n = min(per * p.group - e0, p.cut.chunk(tile));
+  if (part > 0 && n <= 0) return;  // (part 0 writes its zeros)
   extern __shared__ __align__(1024) uint8_t smem[];
   Cta c;
-  if (!cta_begin<D>(c, smem, err)) return;
-  const int kv = blockIdx.x / p.tiles, k0 = (blockIdx.x - kv * p.tiles) * BB;
-  const int k1 = min(k0 + BB, p.w.Nk);
-  const QueryRun run = QueryRun::of(p.w, k0, k1);
-  const int i0 = run.q0 / BB, per = run.q1 > run.q0 ? ceil_div(run.q1, BB) - i0 : 0;
-  const int n = per * p.group;  // query tiles per head, head after head
-  int issued = 0;
+  if (!cta_begin<L>(c, smem, err)) return;
+  int issued_a = 0, issued_b = 0;
 
-  if (c.warp == kLoadWarp) {
-    if (c.lane == 0 && n > 0)
-      issued = load_tiles<D>(c, &tmK, &tmV, k0, kv, &tmQ, &tmO, n, [&](int it, int& head, int& row) {
-        const int g = it / per;
-        head = kv * p.group + g;
-        row = (i0 + it - g * per) * BB;
-      }, err);
-  } else if (c.warp == kMmaWarp) {
-    if (n > 0) {
-      const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0), base = __shfl_sync(0xffffffffu, c.base, 0);
-      const uint64_t dQm = smem_desc_sw128(base + L::kRingA, kSubBytes, 1024);
-      const uint64_t dOm = smem_desc_sw128(base + L::kRingB, kSubBytes, 1024);
-      issue_mmas<D>(c, n, [&](int h, uint64_t off, bool accumulate) {
-        mma_grad_half<D, false>(tmem + kColV, tmem + kColS, dOm + off, h, accumulate);       // dV += P^T dO
-        mma_grad_half<D, false>(tmem + kColK, tmem + kColS + 16, dQm + off, h, accumulate);  // dK += dS^T Q
-      }, err);
+  if (c.warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (c.warp == kLoadWarp) {
+      if (c.lane == 0 && n > 0)
+        load_tiles<D, L>(c, &tmK, &tmV, k0, kv, &tmQ, &tmO, n, [&](int it, int& head, int& row) {
+          const int g = (e0 + it) / per;
+          head = kv * p.group + g;
+          row = (i0 + e0 + it - g * per) * BB;
+        }, issued_a, issued_b, err);
+    } else if (c.warp == kMmaWarp) {
+      if (n > 0) {
+        const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0), base = __shfl_sync(0xffffffffu, c.base, 0);
+        const uint64_t dQm = smem_desc_sw128(base + L::kRingA, kSubBytes, 1024);
+        const uint64_t dOm = smem_desc_sw128(base + L::kRingB, kSubBytes, 1024);
+        issue_mmas<D, 2>(c, n, [&](int h, uint32_t s_col, uint64_t a, uint64_t b, bool accumulate) {
+          mma_grad_half<D, false>(tmem + kColV, tmem + s_col, dOm + b, h, accumulate);       // dV += P^T dO
+          mma_grad_half<D, false>(tmem + kColK, tmem + s_col + 16, dQm + a, h, accumulate);  // dK += dS^T Q
+        }, err);
+      }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElementRegs));
     // thread = key row; columns = the query tile's queries, half h of them
     const int h = c.warp >> 2, row = 32 * (c.warp & 3) + c.lane, wt = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (c.warp & 3)) << 16;
@@ -416,39 +475,41 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2);
     const int u = k0 + row;
     // -lse (base 2) and -delta of this half's 64 queries: threads 0-63 of the
-    // four warps fetch the one, 64-127 the other, a tile pair ahead
-    auto fetch = [&](int it) -> float {
-      const int g = it / per, q = (i0 + it - g * per) * BB + 64 * h + (wt & 63);
+    // four warps fetch the one, 64-127 the other, a tile pair ahead (of query
+    // tile i0 + qi of head g)
+    int g = n > 0 ? e0 / per : 0, qi = e0 - g * per;
+    auto fetch = [&]() -> float {
+      const int q = (i0 + qi) * BB + 64 * h + (wt & 63);
       const size_t tok = (size_t)(kv * p.group + g) * p.w.Nq + q;
       const bool in = q < p.w.Nq;
       if (wt >= 64) return in ? -p.delta[tok] : 0.f;
       const float ls = in ? p.lse[tok] : -INFINITY;
       return ls > -INFINITY ? -ls * kLog2e : -INFINITY;
     };
-    float next = n > 0 ? fetch(0) : 0.f;
+    float next = n > 0 ? fetch() : 0.f;
     bool ok = true;
     for (int it = 0; it < n; ++it) {
-      const int q0 = (i0 + it % per) * BB;
+      const int q0 = (i0 + qi) * BB;
       const bool whole = all_visible(p.w, q0, min(q0 + BB, p.w.Nq), k0, k1);
       float* nl = vec + (it & 1) * 2 * BB;
       float* nd = nl + BB;
       (wt < 64 ? nl : nd)[64 * h + (wt & 63)] = next;
-      if (it + 1 < n) next = fetch(it + 1);
+      if (++qi == per) {
+        qi = 0;
+        ++g;
+      }
+      if (it + 1 < n) next = fetch();
       // the barrier of the half's four warps publishes the values and makes a
       // timed-out wait a decision of all four
-      const bool late = !warp_all(mbar_wait(c.bar(kBarS + h), (uint32_t)it & 1u));
+      const bool late = !warp_all(mbar_wait(c.bar(kBarS + (L::kTwoS ? 0 : h)), (uint32_t)it & 1u));
       if (named_bar_or(1 + h, 128, late)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      const uint32_t s_col = L::s_col(it);
       uint32_t sv[2][32], pv[2][32];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        tmem_ld32(c.tmem + lanes + kColS + 64 * h + 32 * cc, sv[cc]);
-        tmem_ld32(c.tmem + lanes + kColP + 64 * h + 32 * cc, pv[cc]);
-      }
-      read_out(c, h, sv, pv, D == 64);
+      read_half<L>(c, lanes, s_col, h, sv, pv);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const uint32_t col = 64u * h + 32u * cc;
@@ -477,15 +538,15 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           unpack_f32x2(mul_f32x2(pack_f32x2(p0, p1), d2), g0, g1);
           dh[m] = pack_bf16(g0, g1);
         }
-        tmem_st16(c.tmem + lanes + kColS + col, ph);
-        tmem_st16(c.tmem + lanes + kColS + col + 16, dh);
+        tmem_st16(c.tmem + lanes + s_col + col, ph);
+        tmem_st16(c.tmem + lanes + s_col + col + 16, dh);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive(c.bar(kBarP + h));
+      if (c.lane == 0) mbar_arrive(c.bar(kBarP + 2 * (it & 1) + h));
     }
-    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFree + (n - 1) % L::kStages), (uint32_t)((n - 1) / L::kStages) & 1u));
+    if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFreeA + (n - 1) % L::kStagesA), (uint32_t)((n - 1) / L::kStagesA) & 1u));
     if (!ok) {
       give_up(c, err);
     } else {
@@ -502,32 +563,99 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int e = 0; e < 32; ++e) g[e] = 0u;
         }
-        if (u < k1) store_row_chunk(dst + 32 * g32, g, h ? p.scale : 1.0f);
+        if (p.cut.parts(tile) > 1) {  // this CTA's share, for window_join_kernel
+          float4* sh = reinterpret_cast<float4*>(
+              p.shares + ((p.cut.slot(kv, p.tiles, tile, part) * 2 + h) * BB + row) * D + 32 * g32);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            sh[x] = make_float4(__uint_as_float(g[4 * x]), __uint_as_float(g[4 * x + 1]), __uint_as_float(g[4 * x + 2]),
+                                __uint_as_float(g[4 * x + 3]));
+        } else if (u < k1) {
+          store_row_chunk(dst + 32 * g32, g, h ? p.scale : 1.0f);
+        }
       }
     }
   }
-  cta_end<D>(c, n, issued);
+  cta_end<L>(c, n, issued_a, issued_b);
+}
+
+// dK and dV of the tiles that several CTAs share, summed in order: four columns
+// of a row per thread.  Grid: x = heads * tiles that are cut, y = kJoinCtas<D>.
+template <int D>
+constexpr int kJoinCtas = 2 * BB * (D / 4) / 256;
+
+template <int D>
+__global__ void __launch_bounds__(256)
+window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+  const int cut = p.cut.cut_tiles(p.tiles), kv = blockIdx.x / cut, tile = p.cut.cut_tile(blockIdx.x - kv * cut);
+  const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
+  const int n = QueryRun::of(p.w, k0, k1).tiles<BB>() * p.group, parts = max(1, ceil_div(n, p.cut.chunk(tile)));
+  const int i = blockIdx.y * 256 + threadIdx.x, h = i / (BB * (D / 4)), r = i / (D / 4) % BB, d = 4 * (i % (D / 4));
+  if (k0 + r >= k1) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = 0; c < parts; ++c) {
+    const float4 x =
+        *reinterpret_cast<const float4*>(p.shares + ((p.cut.slot(kv, p.tiles, tile, c) * 2 + h) * BB + r) * D + d);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  const float mul = h ? p.scale : 1.f;
+  uint2 o;
+  o.x = pack_bf16(s.x * mul, s.y * mul);
+  o.y = pack_bf16(s.z * mul, s.w * mul);
+  *reinterpret_cast<uint2*>((h ? dk : dv) + ((size_t)kv * p.w.Nk + k0 + r) * D + d) = o;
 }
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                      const WindowAttn& a, cudaStream_t s) {
-  const int smem = Smem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem_q = Layout<D, 1>::kBytes, smem_kv = Layout<D, 2>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(window_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(window_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
   if (e != cudaSuccess) return e;
-  BwdParams p{a.w, a.H / a.Hk, ceil_div(a.w.Nq, BB), a.scale, a.scale * kLog2e, a.lse, a.delta};
-  window_dq_kernel<D><<<a.B * a.H * p.tiles, kThreads, smem, s>>>(mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dq),
+  BwdParams p{a.w,    bwd_chunks(a.B, a.H, a.Hk, a.w), a.shares, a.H / a.Hk, ceil_div(a.w.Nq, BB),
+              a.scale, a.scale * kLog2e,                a.lse,    a.delta};
+  window_dq_kernel<D><<<a.B * a.H * p.tiles, kThreads, smem_q, s>>>(mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dq),
                                                                   a.err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   p.tiles = ceil_div(a.w.Nk, BB);
-  window_dkdv_kernel<D><<<a.B * a.Hk * p.tiles, kThreads, smem, s>>>(
+  window_dkdv_kernel<D><<<a.B * a.Hk * p.cut.ctas(p.tiles), kThreads, smem_kv, s>>>(
       mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dk), static_cast<__nv_bfloat16*>(a.dv), a.err);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (const int cut = p.cut.cut_tiles(p.tiles))
+    window_join_kernel<D><<<dim3(a.B * a.Hk * cut, kJoinCtas<D>), 256, 0, s>>>(
+        p, static_cast<__nv_bfloat16*>(a.dk), static_cast<__nv_bfloat16*>(a.dv));
   return cudaGetLastError();
 }
 
 }  // namespace
+
+// A tile with sinks sees every query, the others a window of them: each kind is
+// cut where its longest tile has more than one and a half times an SM's share of
+// all pairs (a pair takes about 1.5 us, a CTA's start and its share 4 us, so not
+// below eight pairs).
+BwdChunks bwd_chunks(int B, int H, int Hk, const Window& w) {
+  const int tiles = ceil_div(w.Nk, BB), group = H / Hk;
+  BwdChunks c;
+  c.sink_tiles = ceil_div(w.sink, BB);
+  int longest[2] = {0, 0};
+  long long all = 0;
+  for (int t = 0; t < tiles; ++t) {
+    const int n = QueryRun::of(w, t * BB, std::min((t + 1) * BB, w.Nk)).tiles<BB>() * group;
+    all += n;
+    int& l = longest[t >= c.sink_tiles];
+    l = std::max(l, n);
+  }
+  const int share = (int)std::max<long long>(8, (all * B * Hk + 147) / 148);
+  for (int i = 0; i < 2; ++i) {
+    const bool cut = 2ll * longest[i] > 3ll * share;
+    c.chunks[i] = cut ? share : std::max(1, longest[i]);
+    c.counts[i] = cut ? ceil_div(longest[i], share) : 1;
+  }
+  c.heads = B * Hk;
+  return c;
+}
 
 cudaError_t launch_window_bwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why) {
   CUtensorMap mq, mk, mv, mo;

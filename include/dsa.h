@@ -569,8 +569,8 @@ dsa_status dsa_window_attn_fwd(const void* q, const void* k, const void* v, dsa_
  *   workspace  >= dsa_window_attn_bwd_workspace_size(...) bytes, 16-byte
  *              aligned.
  * Every sum has a fixed order: two calls give the same bits.  bf16 runs on
- * tcgen05 with dS as two bf16 terms and P as one; fp32 in exact fp32.
- * Limits as for the forward.
+ * tcgen05, dS as two bf16 terms for dQ, P and dS as one for dV and dK; fp32 in
+ * exact fp32.  Limits as for the forward.
  */
 dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                                const void* dout, const float* lse, dsa_dtype dt, int B, int H,
@@ -579,8 +579,8 @@ dsa_status dsa_window_attn_bwd(const void* q, const void* k, const void* v, cons
                                size_t ws_bytes, void* stream);
 
 /* Device workspace bytes for dsa_window_attn_bwd with these arguments; 0 for
- * invalid sizes.  (The row terms delta; in fp32 also the partial sums of
- * gradient tiles that several CTAs share.) */
+ * invalid sizes.  (The row terms delta, and the partial sums of gradient tiles
+ * that several CTAs share.) */
 size_t dsa_window_attn_bwd_workspace_size(dsa_dtype dt, int B, int H, int Hk, int Nq, int Nk, int D,
                                           int q_offset, int left, int right, int sink);
 

@@ -160,6 +160,17 @@ def test_backward(B, H, Hk, Nq, Nk, D, off, left, right, sink, dtype):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,Hk,Nq,Nk,off,left,right,sink", [
+    (1, 8, 2, 1100, 1100, 0, 150, 0, 130),   # two tiles with sinks, 36 pairs each, against 8 or 12 of the others
+    (1, 8, 1, 1000, 1500, 0, -1, 0, 0),      # 64 pairs down to 8, and the last keys that no query sees
+    (2, 6, 1, 700, 1300, 500, -1, -1, 5),    # both kinds in parts, two batches
+])
+def test_backward_of_key_tiles_in_parts(B, H, Hk, Nq, Nk, off, left, right, sink, D):
+    q, k, v, do = make(B, H, Hk, Nq, Nk, D, torch.bfloat16, seed=Nk)
+    check_backward(q, k, v, do, off, left, right, sink)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_two_query_tiles_per_item(D):
     # more items than SMs, so each item takes two query tiles; the last one has one
     q, k, v, _ = make(1, 160, 20, 390, 390, D, torch.bfloat16, seed=D)

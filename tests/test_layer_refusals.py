@@ -144,6 +144,11 @@ def test_workspace_sizes(lib):
     assert bwd_ws(lib, dt=0) >= bwd_ws(lib)                 # fp32: shares where tiles are few
     # 4 query heads, 16 key tiles of which the first sees every query: dK and dV in shares
     assert bwd_ws(lib, dt=0, Nq=1000, Nk=1000, left=200, sink=3) > 4 * 1000 * 4 + 2 * 2 * 1000 * 64 * 4
+    # bf16: the shares of the one key tile with sinks (64 query tiles of 4 heads against 17 for the others)
+    big = dict(H=16, Hk=4, Nq=8192, Nk=8192, D=128, left=2047)
+    assert bwd_ws(lib, **big) == 16 * 8192 * 4
+    parts = bwd_ws(lib, **big, sink=4) - 16 * 8192 * 4
+    assert parts > 0 and parts % (4 * 2 * 128 * 128 * 4) == 0
     # thousands of tiles: none
     assert bwd_ws(lib, dt=0, H=64, Hk=64, Nq=4096, Nk=4096, left=128) == 64 * 4096 * 4
     need = lib.dsa_window_attn_decode_workspace_size
