@@ -14,16 +14,20 @@ struct BwdChunks {
   __host__ __device__ bool kind(int tile) const { return tile >= sink_tiles; }
   __host__ __device__ int chunk(int tile) const { return kind(tile) ? chunks[1] : chunks[0]; }
   __host__ __device__ int parts(int tile) const { return kind(tile) ? counts[1] : counts[0]; }
-  // CTAs of a head, and what CTA i of them does
+  // CTAs, and what CTA i of them does: the tiles with sinks of all heads come
+  // first, since what is not cut of them takes longest
   __host__ __device__ int ctas(int tiles) const {
-    return sink_tiles * counts[0] + (tiles - sink_tiles) * counts[1];
+    return heads * (sink_tiles * counts[0] + (tiles - sink_tiles) * counts[1]);
   }
-  __host__ __device__ void place(int i, int& tile, int& part) const {
-    const int first = sink_tiles * counts[0], n = i >= first ? counts[1] : counts[0];
-    const int t = i >= first ? sink_tiles : 0;
-    if (i >= first) i -= first;
-    tile = t + i / n;
+  __host__ __device__ void place(int i, int tiles, int& head, int& tile, int& part) const {
+    const int first = heads * sink_tiles * counts[0];
+    const bool k = i >= first;
+    const int n = k ? counts[1] : counts[0], per = k ? tiles - sink_tiles : sink_tiles;
+    if (k) i -= first;
     part = i % n;
+    i /= n;
+    head = i / per;
+    tile = (k ? sink_tiles : 0) + i - head * per;
   }
   // tiles of a head that are cut, and the i-th of them
   __host__ __device__ int cut_tiles(int tiles) const {
@@ -58,6 +62,15 @@ struct WindowAttn {
   int num_sms;
   unsigned* err;
 };
+
+// Order of the query tiles (of all heads): by head, so that CTAs that run at the
+// same time read overlapping windows of few heads, or by tile, the last one
+// first, where the windows of all heads together fit in half of L2.  With a
+// causal mask the first tiles are the shortest, and so the CTAs end together.
+inline bool order_by_tile(const WindowAttn& a) {
+  const int window = a.w.left + a.w.right + 256;
+  return (long long)a.B * a.Hk * (a.w.Nk < window ? a.w.Nk : window) * a.D * 4 <= 60ll << 20;
+}
 
 struct DecodeAttn {
   int B, H, Hk, group, Nq, cap;

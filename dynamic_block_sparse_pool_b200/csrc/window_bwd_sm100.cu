@@ -23,26 +23,27 @@
 // The element-wise pass (eight warps: one row per thread, warps 0-3 the first 64
 // columns, warps 4-7 the others) is what bounds the kernels, so everything else
 // goes on beside it.
-//   dQ: S has two buffers in tensor memory.  While pair e is in its element-wise
-//   pass, S of e + 1 is done already and dP of e + 1 runs as soon as dP of e has
-//   been read; the gradient products of e run, half by half, under the pass of
-//   e + 1, and S of e + 2 follows them into the buffer of e (the MMAs of one
-//   thread run in order).
-//   dK, dV: one buffer; each half's S of e + 1 follows the half's gradient
-//   products of e, so one half's pass goes on while the other half waits.  At
-//   D = 64 dP of e + 1 is done before them, as in dQ; at D = 128, where shared
-//   memory holds two stages of each ring and not three, it follows S.
-// Measured, 17,776 tokens, 8 heads, D = 64, every token in sight of 5,400 others
-// and a prefix of 226: dQ 458 us with two buffers of S, 511 with one; dK/dV 624
-// with one, 644 with two.  8,192 tokens, 16 query heads on 4, D = 128, causal
-// over 2,048: dQ 243 (256 with one), dK/dV 357 with S and dP behind the
-// gradients, 376 with dP ahead of them.
+//   Where tensor memory holds two buffers of S (all but dK/dV at D = 128): while
+//   pair e is in its element-wise pass, S of e + 1 is done already and dP of
+//   e + 1 runs as soon as dP of e has been read; the gradient products of e run
+//   under the pass of e + 1, and S of e + 2 follows them into the buffer of e
+//   (the MMAs of one thread run in order).
+//   With one buffer each half's S and dP of e + 1 follow the half's gradient
+//   products of e, so one half's pass goes on while the other half waits.
 // Warp 8 issues the MMAs, warp 9 the TMA loads into two rings, one for each
 // streamed tensor.  Every mbarrier wait is bounded; a timeout sets the device
 // error word and the CTA winds down.
-// All three kernels with the row terms: 5.2 ms for 17,776 tokens, 48 heads,
-// D = 64, the mask above (545 TFLOP/s); 0.63 ms for the D = 128 shape above with
-// four sinks (475).
+//
+// Measured, 17,776 tokens, 8 heads, D = 64, every token in sight of 5,400 others
+// and a prefix of 226: dQ 430 us (511 with one buffer of S), dK/dV 470 (617);
+// exp2 keeps its unit and the MMAs the tensor cores (N = 64 costs them as much
+// as N = 128) half of the time each, and the two do not overlap in full.  A
+// delay of half the warps by a third of a pass, so that one half computes while
+// the other reads, costs 5 %.  48 heads: 4.8 ms in all (590 TFLOP/s).
+// 8,192 tokens, 16 query heads on 4, D = 128, causal over 2,048, four sinks: dQ
+// 229 us, dK/dV 270 (357 with the sinks' tile uncut and last, 376 with dP ahead
+// of the gradients), 0.52 ms in all (575 TFLOP/s); causal without a window
+// 1.03 ms (667).
 #include <algorithm>
 
 #include "bwd_tiles.cuh"
@@ -58,33 +59,32 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 // warps 10 and 11 only fill up the third warpgroup: of its registers (168 a thread
 // at launch) the element-wise warps take what it does not need
-// (5.29 -> 5.19 ms at D = 64, 0.62 -> 0.63 at D = 128, the shapes above)
+// (2 % at D = 64, where dK/dV else spills)
 constexpr int kElementRegs = 208, kOtherRegs = 88;
 static_assert(256 * kElementRegs + 128 * kOtherRegs <= 168 * kThreads);
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Barriers, with room for three stages of each ring.  kBarS (+ half, with one
-// buffer of S): S and dP of a pair are done; kBarR: dP is read out of tensor
-// memory (eight warps; where dP of the next pair comes early); kBarP + 2 (pair % 2) + half: the half's terms are written
-// (four warps).  With two buffers of S a warp may be done with pair e + 1 before
-// another one is with e, so their arrivals must not meet on one barrier; e + 2 it
-// cannot reach, since S and dP of it wait for every warp's kBarR of e + 1.
+// buffer of S): S and dP of a pair are done; kBarR, with two buffers: dP is read
+// out of tensor memory (eight warps); kBarP + 2 (pair % 2) (+ half, with one): the
+// terms are written.  With two buffers of S a warp may be done with pair e + 1
+// before another one is with e, so their arrivals must not meet on one barrier;
+// e + 2 it cannot reach, since S and dP of it wait for every warp's kBarR of e + 1.
 enum : int { kBarFixed = 0, kBarRingA = 1, kBarRingB = 4, kBarFreeA = 7, kBarFreeB = 10, kBarS = 13, kBarR = 15,
              kBarP = 16, kBarDrain = 20, kNumBars = 21 };
 
 // Tensor and shared memory of a kernel with NG gradient accumulators.  The
 // streamed tile A is read by S and by a gradient product, two pairs apart where
 // S has two buffers; B by dP and, with NG = 2, by a gradient product.  A tile
-// that is needed before the gradient products of the pair before has a third
-// stage, so that its load does not wait for them.
+// that is needed before the gradient products of the pair before it are done has
+// a third stage, so that its load does not wait for them.
 template <int D, int NG>
 struct Layout {
-  static constexpr bool kTwoS = NG == 1;
-  static constexpr bool kEarlyP = NG == 1 || D == 64;  // dP of the next pair before the gradient products
+  static constexpr bool kTwoS = 3 * BB + NG * D <= (int)kTmemCols;
   static constexpr uint32_t kColP = kTwoS ? 2 * BB : BB, kColG = kColP + BB;  // dP, gradients (S at 0)
   static constexpr int kTile = BB * D * 2;
-  static constexpr int kStagesA = kEarlyP ? 3 : 2, kStagesB = kEarlyP && NG == 2 ? 3 : 2;
+  static constexpr int kStagesA = kTwoS ? 3 : 2, kStagesB = kTwoS && NG == 2 ? 3 : 2;
   static constexpr int kFixA = 0, kFixB = kTile;          // the CTA's own two tiles
   static constexpr int kRingA = 2 * kTile;
   static constexpr int kRingB = kRingA + kStagesA * kTile;
@@ -103,6 +103,8 @@ struct BwdParams {
   int tiles;       // tiles per head of the CTA's side
   float scale, scale_log2;
   const float *lse, *delta;
+  int heads;       // dq: B H
+  bool by_tile;    // dq: order_by_tile
 };
 
 // bits 0 .. v-1
@@ -132,7 +134,7 @@ __device__ __forceinline__ bool cta_begin(Cta& c, uint8_t* smem, unsigned* err) 
   c.abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
   if (c.warp == kMmaWarp) {
     if (c.lane == 0) {
-      for (int i = 0; i < kNumBars; ++i) mbar_init(c.bar(i), i == kBarR ? 8u : i >= kBarP && i < kBarP + 4 ? 4u : 1u);
+      for (int i = 0; i < kNumBars; ++i) mbar_init(c.bar(i), i == kBarR ? 8u : i >= kBarP && i < kBarP + 4 ? (L::kTwoS ? 8u : 4u) : 1u);
       *c.abort_flag = 0;
       fence_mbar_init();
     }
@@ -195,7 +197,7 @@ __device__ __forceinline__ void read_half(const Cta& c, uint32_t lanes, uint32_t
     tmem_wait_ld_regs(sv[cc]);
     tmem_wait_ld_regs(pv[cc]);
   }
-  if (L::kEarlyP) {
+  if (L::kTwoS) {
     tc_fence_before();
     __syncwarp();
     if (c.lane == 0) mbar_arrive(c.bar(kBarR));
@@ -234,8 +236,8 @@ __device__ __forceinline__ void load_tiles(const Cta& c, const CUtensorMap* fa, 
 }
 
 // The MMA issuer's part: S = A a^T and dP = B b^T (A, B fixed, a, b streamed),
-// and `grads(half, column of S, stage of a, stage of b, accumulate)` once a
-// half's terms are written.
+// and `grads(half, column of S, stage of a, stage of b, accumulate)` once the
+// terms are written.
 template <int D, int NG, typename Grads>
 __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, unsigned* err) {
   using L = Layout<D, NG>;
@@ -272,45 +274,55 @@ __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, uns
   }
   for (int it = 0; it < n && ok; ++it) {
     const bool more = it + 1 < n;
-    if (L::kEarlyP && more) {
-      if (!(ok = warp_all(mbar_wait_both(c.bar(kBarRingB + (it + 1) % L::kStagesB),
-                                         (uint32_t)((it + 1) / L::kStagesB) & 1u, c.bar(kBarR), (uint32_t)it & 1u))))
-        break;
-      tc_fence_after();
-      if (elect_one()) {
-        dprobs(it + 1);
-        if (L::kTwoS) mma_commit(c.bar(kBarS));
-        if (NG == 1) mma_commit(c.bar(kBarFreeB + (it + 1) % L::kStagesB));
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!(ok = ok && warp_all(mbar_wait(c.bar(kBarP + 2 * (it & 1) + h), (uint32_t)(it >> 1) & 1u)))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        grads(h, L::s_col(it), stage_a(it), stage_b(it), it > 0 || h > 0);
-        if (h == 1) mma_commit(c.bar(kBarFreeA + it % L::kStagesA));
-        if (h == 1 && NG == 2) mma_commit(c.bar(kBarFreeB + it % L::kStagesB));
-      }
-      __syncwarp();
-      if (!L::kTwoS && more) {  // the half's S follows at once
-        if (h == 0 && !(ok = landed(kBarRingA, it + 1, L::kStagesA) &&
-                             (L::kEarlyP || landed(kBarRingB, it + 1, L::kStagesB))))
+    if constexpr (L::kTwoS) {
+      if (more) {
+        if (!(ok = warp_all(mbar_wait_both(c.bar(kBarRingB + (it + 1) % L::kStagesB),
+                                           (uint32_t)((it + 1) / L::kStagesB) & 1u, c.bar(kBarR), (uint32_t)it & 1u))))
           break;
+        tc_fence_after();
         if (elect_one()) {
-          mma_rows_half<D>(tmem + 64 * h, dA, da + stage_a(it + 1), h);
-          if (!L::kEarlyP) mma_rows_half<D>(tmem + L::kColP + 64 * h, dB, db + stage_b(it + 1), h);
-          mma_commit(c.bar(kBarS + h));
+          dprobs(it + 1);
+          mma_commit(c.bar(kBarS));
+          if (NG == 1) mma_commit(c.bar(kBarFreeB + (it + 1) % L::kStagesB));
         }
         __syncwarp();
       }
-    }
-    if (!ok) break;
-    if (L::kTwoS && it + 2 < n) {
-      if (!(ok = landed(kBarRingA, it + 2, L::kStagesA))) break;
-      if (elect_one()) scores(it + 2);
+      const uint32_t done = c.bar(kBarP + 2 * (it & 1)), parity = (uint32_t)(it >> 1) & 1u;
+      const bool ahead = it + 2 < n;
+      if (!(ok = warp_all(ahead ? mbar_wait_both(c.bar(kBarRingA + (it + 2) % L::kStagesA),
+                                                 (uint32_t)((it + 2) / L::kStagesA) & 1u, done, parity)
+                                : mbar_wait(done, parity))))
+        break;
+      tc_fence_after();
+      if (elect_one()) {
+        grads(0, L::s_col(it), stage_a(it), stage_b(it), it > 0);
+        grads(1, L::s_col(it), stage_a(it), stage_b(it), true);
+        mma_commit(c.bar(kBarFreeA + it % L::kStagesA));
+        if (NG == 2) mma_commit(c.bar(kBarFreeB + it % L::kStagesB));
+        if (ahead) scores(it + 2);
+      }
       __syncwarp();
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(ok = ok && warp_all(mbar_wait(c.bar(kBarP + 2 * (it & 1) + h), (uint32_t)(it >> 1) & 1u)))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          grads(h, 0u, stage_a(it), stage_b(it), it > 0 || h > 0);
+          if (h == 1) mma_commit(c.bar(kBarFreeA + it % L::kStagesA));
+          if (h == 1) mma_commit(c.bar(kBarFreeB + it % L::kStagesB));
+        }
+        __syncwarp();
+        if (more) {  // the half's S and dP follow at once
+          if (h == 0 && !(ok = landed(kBarRingA, it + 1, L::kStagesA) && landed(kBarRingB, it + 1, L::kStagesB))) break;
+          if (elect_one()) {
+            mma_rows_half<D>(tmem + 64 * h, dA, da + stage_a(it + 1), h);
+            mma_rows_half<D>(tmem + L::kColP + 64 * h, dB, db + stage_b(it + 1), h);
+            mma_commit(c.bar(kBarS + h));
+          }
+          __syncwarp();
+        }
+      }
     }
   }
   if (!ok) give_up(c, err);
@@ -325,7 +337,8 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   extern __shared__ __align__(1024) uint8_t smem[];
   Cta c;
   if (!cta_begin<L>(c, smem, err)) return;
-  const int bh = blockIdx.x / p.tiles, q0 = (blockIdx.x - bh * p.tiles) * BB;
+  const int run = p.by_tile ? p.heads : p.tiles, o = blockIdx.x / run, r = blockIdx.x - o * run;
+  const int bh = p.by_tile ? r : o, q0 = (p.tiles - 1 - (p.by_tile ? o : r)) * BB;
   const int q1 = min(q0 + BB, p.w.Nq);
   const KeyTiles<BB> kt = KeyTiles<BB>::of(p.w, q0, q1);
   const int n = kt.count();
@@ -399,7 +412,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive(c.bar(kBarP + 2 * (it & 1) + h));
+      if (c.lane == 0) mbar_arrive(c.bar(kBarP + 2 * (it & 1) + (L::kTwoS ? 0 : h)));
     }
     if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFreeA + (n - 1) % L::kStagesA), (uint32_t)((n - 1) / L::kStagesA) & 1u));
     if (!ok) {
@@ -432,9 +445,8 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                    __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, unsigned* err) {
   using L = Layout<D, 2>;
   constexpr uint32_t kColV = L::kColG, kColK = L::kColG + D;
-  const int ctas = p.cut.ctas(p.tiles), kv = blockIdx.x / ctas;
-  int tile, part;
-  p.cut.place(blockIdx.x - kv * ctas, tile, part);
+  int kv, tile, part;
+  p.cut.place(blockIdx.x, p.tiles, kv, tile, part);
   const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
   const QueryRun run = QueryRun::of(p.w, k0, k1);
   const int i0 = run.q0 / BB, per = run.tiles<BB>();
@@ -478,13 +490,13 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // four warps fetch the one, 64-127 the other, a tile pair ahead (of query
     // tile i0 + qi of head g)
     int g = n > 0 ? e0 / per : 0, qi = e0 - g * per;
+    // what is loaded is touched a pair later only: the load's latency stays hidden
+    const float* src = wt < 64 ? p.lse : p.delta;
     auto fetch = [&]() -> float {
       const int q = (i0 + qi) * BB + 64 * h + (wt & 63);
-      const size_t tok = (size_t)(kv * p.group + g) * p.w.Nq + q;
-      const bool in = q < p.w.Nq;
-      if (wt >= 64) return in ? -p.delta[tok] : 0.f;
-      const float ls = in ? p.lse[tok] : -INFINITY;
-      return ls > -INFINITY ? -ls * kLog2e : -INFINITY;
+      float x = wt < 64 ? -INFINITY : 0.f;
+      if (q < p.w.Nq) x = src[(size_t)(kv * p.group + g) * p.w.Nq + q];
+      return x;
     };
     float next = n > 0 ? fetch() : 0.f;
     bool ok = true;
@@ -493,7 +505,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const bool whole = all_visible(p.w, q0, min(q0 + BB, p.w.Nq), k0, k1);
       float* nl = vec + (it & 1) * 2 * BB;
       float* nd = nl + BB;
-      (wt < 64 ? nl : nd)[64 * h + (wt & 63)] = next;
+      (wt < 64 ? nl : nd)[64 * h + (wt & 63)] = wt >= 64 ? -next : next > -INFINITY ? -next * kLog2e : -INFINITY;
       if (++qi == per) {
         qi = 0;
         ++g;
@@ -544,7 +556,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive(c.bar(kBarP + 2 * (it & 1) + h));
+      if (c.lane == 0) mbar_arrive(c.bar(kBarP + 2 * (it & 1) + (L::kTwoS ? 0 : h)));
     }
     if (ok && n > 0) ok = warp_all(mbar_wait(c.bar(kBarFreeA + (n - 1) % L::kStagesA), (uint32_t)((n - 1) / L::kStagesA) & 1u));
     if (!ok) {
@@ -615,12 +627,13 @@ cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   e = cudaFuncSetAttribute(window_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
   if (e != cudaSuccess) return e;
   BwdParams p{a.w,    bwd_chunks(a.B, a.H, a.Hk, a.w), a.shares, a.H / a.Hk, ceil_div(a.w.Nq, BB),
-              a.scale, a.scale * kLog2e,                a.lse,    a.delta};
+              a.scale, a.scale * kLog2e,                a.lse,    a.delta,   a.B * a.H,
+              order_by_tile(a)};
   window_dq_kernel<D><<<a.B * a.H * p.tiles, kThreads, smem_q, s>>>(mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dq),
                                                                   a.err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   p.tiles = ceil_div(a.w.Nk, BB);
-  window_dkdv_kernel<D><<<a.B * a.Hk * p.cut.ctas(p.tiles), kThreads, smem_kv, s>>>(
+  window_dkdv_kernel<D><<<p.cut.ctas(p.tiles), kThreads, smem_kv, s>>>(
       mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dk), static_cast<__nv_bfloat16*>(a.dv), a.err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (const int cut = p.cut.cut_tiles(p.tiles))

@@ -2,9 +2,9 @@
 (csrc/window_bwd_sm100.cu), on the CPU: the loader, the MMA issuer and the eight
 element-wise warps as generators that wait on mbarriers by parity and work for
 random times, with a check at every access that a buffer holds what it should.
-The three layouts of the kernels (dQ: two buffers of S; dK and dV: one, with dP
-of the next pair early in one piece, or half by half behind the gradient
-products) must hold under random timing;
+The layouts of the kernels (two buffers of S, with one or two gradient products
+per pair; one buffer, with S and dP half by half behind them) must hold under
+random timing;
 planted mistakes must be caught, among them the terms of both pairs in flight
 signalled on one barrier, as the kernel first had it: a warp that ran ahead
 then stood in for one that had not written yet."""
@@ -15,10 +15,10 @@ import pytest
 from test_window_fwd_protocol_model import Bar, Sim, Stuck, Wrong
 
 
-LAYOUTS = {  # two buffers of S, dP early, gradients per pair, stages of the two rings
-    "dq": (True, True, 1, 3, 2),
-    "dkdv64": (False, True, 2, 3, 3),
-    "dkdv128": (False, False, 2, 2, 2),
+LAYOUTS = {  # two buffers of S, gradients per pair, stages of the two rings
+    "dq": (True, 1, 3, 2),
+    "dkdv64": (True, 2, 3, 3),
+    "dkdv128": (False, 2, 2, 2),
 }
 
 
@@ -26,7 +26,7 @@ class Bwd(Sim):
     def __init__(self, seed, n, layout, mistake=None):
         super().__init__(seed, [], 1, None)
         self.n, self.mistake = n, mistake
-        self.two, self.early, self.ng, self.NA, self.NB = LAYOUTS[layout]
+        self.two, self.ng, self.NA, self.NB = LAYOUTS[layout]
         self.bar = {"fixed": Bar(1)}
         for r, k in (("a", self.NA), ("b", self.NB)):
             for i in range(k):
@@ -34,7 +34,7 @@ class Bwd(Sim):
         for h in (0, 1):
             self.bar["s", h] = Bar(1)
             for p in (0, 1):
-                self.bar["p", p, h] = Bar(4)
+                self.bar["p", p, h] = Bar(8 if self.two else 4)  # two buffers: h = 0 for all
         self.bar["r"] = Bar(8)
         self.hold = {"a": [None] * self.NA, "b": [None] * self.NB}
         self.busy = {"a": [0] * self.NA, "b": [0] * self.NB}
@@ -138,39 +138,45 @@ class Bwd(Sim):
             yield "wait", ("full", "a", 1 % self.NA), (1 // self.NA) & 1
             self.scores(1, (0, 1))
         for it in range(self.n):
-            more = it + 1 < self.n
-            if self.early and more:
-                yield "wait", ("full", "b", (it + 1) % self.NB), ((it + 1) // self.NB) & 1
-                if self.mistake != "no_read_wait":
-                    yield "wait", "r", it & 1
-                self.dprobs(it + 1)
-                if self.two:
+            more, p, ph = it + 1 < self.n, it & 1, (it >> 1) & 1
+            if self.mistake == "one_p":
+                p, ph = 0, it & 1
+            if self.two:
+                if more:
+                    yield "wait", ("full", "b", (it + 1) % self.NB), ((it + 1) // self.NB) & 1
+                    if self.mistake != "no_read_wait":
+                        yield "wait", "r", it & 1
+                    self.dprobs(it + 1)
                     self.sign(("s", 0))
-                if self.ng == 1:
-                    self.sign(("free", "b", (it + 1) % self.NB))
+                    if self.ng == 1:
+                        self.sign(("free", "b", (it + 1) % self.NB))
+                    yield self.rnd(100)
+                if it + 2 < self.n:
+                    yield "wait", ("full", "a", (it + 2) % self.NA), ((it + 2) // self.NA) & 1
+                yield "wait", ("p", p, 0), ph
+                self.grads(it, 0)
+                self.grads(it, 1)
+                self.sign(("free", "a", it % self.NA))
+                if self.ng == 2:
+                    self.sign(("free", "b", it % self.NB))
+                if it + 2 < self.n:
+                    self.scores(it + 2, (0, 1))
                 yield self.rnd(100)
+                continue
             for h in (0, 1):
-                p, ph = (0, it & 1) if self.mistake == "one_p" else (it & 1, (it >> 1) & 1)
                 yield "wait", ("p", p, h), ph
                 self.grads(it, h)
                 if h == 1:
                     self.sign(("free", "a", it % self.NA))
-                    if self.ng == 2:
-                        self.sign(("free", "b", it % self.NB))
+                    self.sign(("free", "b", it % self.NB))
                 yield self.rnd(150)
-                if not self.two and more:
+                if more:
                     if h == 0:
                         yield "wait", ("full", "a", (it + 1) % self.NA), ((it + 1) // self.NA) & 1
-                        if not self.early:
-                            yield "wait", ("full", "b", (it + 1) % self.NB), ((it + 1) // self.NB) & 1
+                        yield "wait", ("full", "b", (it + 1) % self.NB), ((it + 1) // self.NB) & 1
                     self.scores(it + 1, (h,))
-                    if not self.early:
-                        self.dprobs(it + 1, (h,))
+                    self.dprobs(it + 1, (h,))
                     self.sign(("s", h))
-            if self.two and it + 2 < self.n:
-                yield "wait", ("full", "a", (it + 2) % self.NA), ((it + 2) // self.NA) & 1
-                self.scores(it + 2, (0, 1))
-                yield self.rnd(100)
 
     def warp(self, w):
         h = w // 4
@@ -182,13 +188,13 @@ class Bwd(Sim):
             if self.dp[h] != it:
                 raise Wrong("dP changed while it was read")
             self.reads[it, h] = self.reads.get((it, h), 0) + 1
-            if self.early:
+            if self.two:
                 self.arrive("r")
             yield self.rnd(1200 * (4 if self.rng.random() < 0.05 else 1))  # now and then a slow warp
             if self.sbuf[self.sb(it), h] != ("S", it):
                 raise Wrong("S gone before its terms were written")
             self.written[it, h] = self.written.get((it, h), 0) + 1
-            self.arrive(("p", 0 if self.mistake == "one_p" else it & 1, h))
+            self.arrive(("p", 0 if self.mistake == "one_p" else it & 1, 0 if self.two else h))
         yield "wait", ("free", "a", (self.n - 1) % self.NA), ((self.n - 1) // self.NA) & 1
         if self.done_pairs != self.n:
             raise Wrong(f"output after {self.done_pairs} of {self.n} pairs")
