@@ -8,19 +8,28 @@
 //             with h = x r and m = mean(g w h):  dx = r (g w - h m).
 // All in fp32 from the loaded values, rounded once at the store.
 //
-// Bound by memory (about 3 to 4 operations per byte): every row is read once
-// and written once, so nothing but the layout is left to choose.  x is
+// Bound by memory (about 3 to 4 operations per byte), and where rows are held
+// in 8 bits by instruction issue as well: every row is read once and written
+// once, so the layout and the instruction count are left to choose.  x is
 // token-major (strided: the fused projection's output is read in place), y
 // is head-major, and the rotation depends on the token alone, so a warp
 // keeps one token: it fetches the token's cosines and sines once (from small
 // per-axis tables that stay in L1) and runs over the token's heads, D / 8
 // threads of eight values per row.  Reads are whole token rows; writes are
 // one row per head, next to those of the seven tokens of the CTA's other
-// warps.  kUnroll rows per thread are in flight to cover the latency of HBM.
+// warps.  The loads that cover the latency of HBM: four rows per thread in
+// registers (forward), asynchronous copies three steps ahead (backward, where
+// the sums of dw need the registers).
 //
 // x may be 8-bit rows (codes and scales, rows8.cuh) in place of bf16 or fp32,
 // and the forward can write those of x beside y, so a training step keeps a
 // byte per value where it kept two and reads less in the backward.
+//
+// Measured, D = 128, bf16, counted bytes (each value once): 118,800 tokens, 24 +
+// 24 heads: forward 469 us (6.2 TB/s), saving codes 646 (5.6), from codes 424
+// (5.2), backward 697 (6.3), from codes 740 (4.9); there 65 to 80 % of the issue
+// slots are taken.  75,600 tokens, 40 + 40 heads: forward 506 us (6.1).  D = 64,
+// 17,776 tokens, 48 + 48 heads: backward 120 us (5.5).
 #include <algorithm>
 
 #include "norm_rope.cuh"
@@ -34,12 +43,15 @@ using namespace rows8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// The turn of a thread's eight values, as y = x c + partner(x) s with the
-// signs in s.  Neighbouring pairs: the partner is the other value of the pair.
-// Halves: it is the same value of the thread D / 16 further on.
+// The turn of a thread's eight values, as y = x c + partner(x) s.  Neighbouring
+// pairs: the partner is the other value of the pair (single operations: the
+// packed ones would need a swapped copy of every pair, which costs what they
+// save).  Halves: it is the same value of the thread D / 16 further on, and the
+// signs are in s.
 template <int D, bool HALVES>
 struct Turn {
-  Pair c[4], s[4];
+  Pair c[4], s[4];      // halves
+  float c1[4], s1[4];   // neighbours
 
   // The token's angles from the tables.  A position below 0 does not turn;
   // one past its axis' table is reported and does not turn either.
@@ -85,28 +97,30 @@ struct Turn {
     } else {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        c[m] = both(t[m].x);
-        s[m] = pair(-t[m].y, t[m].y);
+        c1[m] = t[m].x;
+        s1[m] = t[m].y;
       }
     }
   }
   // The opposite turn.
   __device__ __forceinline__ void reverse() {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) s[m] = mul_f32x2(s[m], both(-1.f));
+    for (int m = 0; m < 4; ++m) {
+      if (HALVES) s[m] = mul_f32x2(s[m], both(-1.f));
+      else s1[m] = -s1[m];
+    }
   }
   __device__ __forceinline__ void apply(Pair (&v)[4]) const {
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      Pair o;
+      float x, y;
+      unpack_f32x2(v[m], x, y);
       if (HALVES) {
-        float x, y;
-        unpack_f32x2(v[m], x, y);
-        o = pair(__shfl_xor_sync(0xffffffffu, x, D / 16), __shfl_xor_sync(0xffffffffu, y, D / 16));
+        const Pair o = pair(__shfl_xor_sync(0xffffffffu, x, D / 16), __shfl_xor_sync(0xffffffffu, y, D / 16));
+        v[m] = fma_f32x2(v[m], c[m], mul_f32x2(o, s[m]));
       } else {
-        o = swapped(v[m]);
+        v[m] = pair(fmaf(x, c1[m], -(y * s1[m])), fmaf(y, c1[m], x * s1[m]));
       }
-      v[m] = fma_f32x2(v[m], c[m], mul_f32x2(o, s[m]));
     }
   }
 };
@@ -150,7 +164,7 @@ struct FwdArgs {
 };
 
 // Grid: x = tokens / 8 (one warp per token), y = parts of the token's heads.
-// A step is kUnroll * (32 / TPR) heads of q or of k.
+// A step is UNROLL * (32 / TPR) heads of q or of k.
 template <typename TIn, typename TOut, int D, bool HALVES, bool SAVE8, int UNROLL>
 __global__ void __launch_bounds__(kThreads, sizeof(TIn) == 4 ? 3 : 4)
 qk_norm_rope_kernel(const FwdArgs<TIn, TOut> a) {
@@ -185,6 +199,13 @@ qk_norm_rope_kernel(const FwdArgs<TIn, TOut> a) {
     }
     if (st == s0) turn.load(a.rope, b, n, sub, a.err);
     if (st == s0 || st == steps_q) load_weight(side.w, sub, w);
+    float inv[UNROLL], save = 0.f;
+    if constexpr (SAVE8) {
+      uint32_t top[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) top[u] = row_top<TPR>(top_bits(raw[u]));
+      save = scales8<TPR>(top, sub, inv);
+    }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int h = h0 + u * RPW;
@@ -194,12 +215,10 @@ qk_norm_rope_kernel(const FwdArgs<TIn, TOut> a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) ss = fma_f32x2(v[m], v[m], ss);
       if constexpr (SAVE8) {
-        float scale;
-        const uint2 c = encode8(v, row_top<TPR>(top_bits(raw[u])), scale);
         if (h < heads) {
           const long long row = (long long)token * heads + h;
-          *reinterpret_cast<uint2*>((is_k ? a.ck : a.cq) + row * D + 8 * sub) = c;
-          if (sub == 0) (is_k ? a.sk : a.sq)[row] = scale;
+          *reinterpret_cast<uint2*>((is_k ? a.ck : a.cq) + row * D + 8 * sub) = encode8(v, inv[u]);
+          if (sub == 2 * u) (is_k ? a.sk : a.sq)[row] = save;
         }
       }
       // (8-bit rows: v holds the codes, the row is scale * v)

@@ -24,11 +24,6 @@ namespace rows8 {
 typedef uint64_t Pair;
 __device__ __forceinline__ Pair pair(float lo, float hi) { return pack_f32x2(lo, hi); }
 __device__ __forceinline__ Pair both(float v) { return pack_f32x2(v, v); }
-__device__ __forceinline__ Pair swapped(Pair p) {
-  float a, b;
-  unpack_f32x2(p, a, b);
-  return pack_f32x2(b, a);
-}
 __device__ __forceinline__ float added(Pair p) {
   float a, b;
   unpack_f32x2(p, a, b);
@@ -155,18 +150,26 @@ __device__ __forceinline__ uint32_t row_top(uint32_t top) {
   return top;
 }
 
-// A thread's codes and the row's scale, from the row's largest magnitude (see
-// above).
-__device__ __forceinline__ uint2 encode8(const Pair (&x)[4], uint32_t top, float& scale) {
-  const float amax = __uint_as_float(top);
-  float inv = 0.f;
-  scale = 0.f;
-  if (top >= 0x7f800000u) {
-    scale = __uint_as_float(0x7fc00000u);
-  } else if (amax >= 0x1p-119f) {
-    scale = __fdiv_rn(amax, 127.0f);
-    inv = __fdiv_rn(127.0f, amax);
-  }
+// Scales of U rows, from the rows' largest magnitudes (see above): thread 2 u of
+// a row's threads returns row u's scale, amax / 127, and inv[u] = 127 / amax is
+// for all of them.  (2 U threads make one division each, so that 2 U divisions
+// cost the issue slots of one.)
+template <int TPR, int U>
+__device__ __forceinline__ float scales8(const uint32_t (&top)[U], int sub, float (&inv)[U]) {
+  static_assert(2 * U <= TPR);
+  uint32_t t = top[0];
+#pragma unroll
+  for (int u = 1; u < U; ++u) t = (sub >> 1) == u ? top[u] : t;
+  const float amax = __uint_as_float(t);
+  const bool some = t < 0x7f800000u && amax >= 0x1p-119f;
+  float q = some ? __fdiv_rn(sub & 1 ? 127.0f : amax, sub & 1 ? amax : 127.0f) : 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) inv[u] = __shfl_sync(0xffffffffu, q, 2 * u + 1, TPR);
+  return t >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q;
+}
+
+// A thread's codes of a row with inv = 127 / amax.
+__device__ __forceinline__ uint2 encode8(const Pair (&x)[4], float inv) {
   // round-half-even by the adder: 1.5 * 2^23 + v keeps the integer nearest to v
   // (ties to even) in its low bits, here the low byte as |v| <= 127
   uint32_t t[8];
