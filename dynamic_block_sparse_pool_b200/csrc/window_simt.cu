@@ -284,35 +284,33 @@ window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k
   stage<D>(K, k + kh, k0, w.Nk);
   stage<D>(V, v + kh, k0, w.Nk);
   float ak[4][D / 16] = {}, av[4][D / 16] = {};
-  {
-    for (int e = e0; e < e1; ++e) {
-      const int h = e / per, q0 = (i0 + e - h * per) * T;
-      const size_t bh = (size_t)kv * group + h, qh = bh * w.Nq * D;
-      __syncthreads();
-      stage<D>(Q, q + qh, q0, w.Nq);
-      stage<D>(O, dout + qh, q0, w.Nq);
-      stage_vec(ls, lse + bh * w.Nq, q0, w.Nq, -INFINITY);
-      stage_vec(de, delta + bh * w.Nq, q0, w.Nq, 0.f);
-      __syncthreads();
-      float s[4][4] = {}, dp[4][4] = {}, p[4][4], ds[4][4];
-      product_nt<D>(s, Q, K, ty, tx);
-      product_nt<D>(dp, O, V, ty, tx);
-      weights(s, dp, p, ds, w, q0, k0, all_visible(w, q0, min(q0 + T, w.Nq), k0, k0 + T), scale, ls, de, ty, tx);
-      // transposed into shared memory: row = key
+  for (int e = e0; e < e1; ++e) {
+    const int h = e / per, q0 = (i0 + e - h * per) * T;
+    const size_t bh = (size_t)kv * group + h, qh = bh * w.Nq * D;
+    __syncthreads();
+    stage<D>(Q, q + qh, q0, w.Nq);
+    stage<D>(O, dout + qh, q0, w.Nq);
+    stage_vec(ls, lse + bh * w.Nq, q0, w.Nq, -INFINITY);
+    stage_vec(de, delta + bh * w.Nq, q0, w.Nq, 0.f);
+    __syncthreads();
+    float s[4][4] = {}, dp[4][4] = {}, p[4][4], ds[4][4];
+    product_nt<D>(s, Q, K, ty, tx);
+    product_nt<D>(dp, O, V, ty, tx);
+    weights(s, dp, p, ds, w, q0, k0, all_visible(w, q0, min(q0 + T, w.Nq), k0, k0 + T), scale, ls, de, ty, tx);
+    // transposed into shared memory: row = key
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = p[a][b];
-      __syncthreads();
-      product_nn<D>(av, W, O, ty, tx);
-      __syncthreads();
+      for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = p[a][b];
+    __syncthreads();
+    product_nn<D>(av, W, O, ty, tx);
+    __syncthreads();
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = ds[a][b];
-      __syncthreads();
-      product_nn<D>(ak, W, Q, ty, tx);
-    }
+      for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = ds[a][b];
+    __syncthreads();
+    product_nn<D>(ak, W, Q, ty, tx);
   }
   float one[4] = {1.f, 1.f, 1.f, 1.f}, mul[4] = {scale, scale, scale, scale};
   store_rows<D>(dv + share + kh, av, k0, k1, one, ty, tx);

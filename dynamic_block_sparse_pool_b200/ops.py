@@ -308,6 +308,18 @@ class HilbertOrder:
 
 # ------------------------------------------------- around the attention --
 
+def _check_workspace(ws: torch.Tensor, t: torch.Tensor) -> None:
+    if ws.device != t.device or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+
+
+def _int32(what: str, v) -> int:
+    v = int(v)
+    if not -2**31 <= v < 2**31:  # ctypes would take the low 32 bits
+        raise ValueError(f"{what} = {v} does not fit in 32 bits")
+    return v
+
+
 class Act8(NamedTuple):
     """Activation rows of D values in 8 bits: the value held is code * scale."""
 
@@ -359,9 +371,12 @@ def unpack8(a: Act8, dtype: torch.dtype = torch.bfloat16,
 
 def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None) -> torch.Tensor:
     """fp32 [positions, pairs, 2] on the device: cos and sin of p * theta^(-i / pairs)."""
+    positions, pairs = _int32("positions", positions), _int32("pairs", pairs)
     if positions < 1 or pairs < 1:
         raise ValueError("positions and pairs must be at least 1")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError(f"the rotation tables live on a CUDA device, not on {dev}")
     t = torch.empty(positions, pairs, 2, dtype=torch.float32, device=dev)
     with _on(t):
         st = lib().dsa_rope_table(positions, pairs, float(theta), t.data_ptr(), _stream(t))
@@ -408,6 +423,8 @@ class RopePlan:
     def _positions(pos: torch.Tensor, dev) -> torch.Tensor:
         if pos.dim() not in (2, 3) or not 1 <= pos.shape[-1] <= 3 or pos.is_floating_point():
             raise ValueError("pos must be integers [N, axes] or [B, N, axes], up to three axes")
+        if pos.dtype == torch.int64:  # what 32 bits cannot hold stays past every table
+            pos = pos.clamp(-1, 2**31 - 1)
         pos = pos.to(device=dev, dtype=torch.int32)
         if pos.shape[-1] < 3:
             pos = torch.nn.functional.pad(pos, (0, 3 - pos.shape[-1]), value=-1)
@@ -543,6 +560,7 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, xq, xk, wq: Optional[to
         return dxq, dxk, dwq.zero_(), dwk.zero_()
     if workspace is None:
         workspace = dq.new_empty(int(lib().dsa_qk_norm_rope_bwd_workspace_size(D)), dtype=torch.uint8)
+    _check_workspace(workspace, dq)
     with _on(dq):
         st = lib().dsa_qk_norm_rope_bwd(
             dq.data_ptr(), dk.data_ptr(), vq.data_ptr(), vk.data_ptr(), _ptr(sq), _ptr(sk), st6,
@@ -578,6 +596,10 @@ def _check_lse(lse, q):
         raise ValueError("lse must be contiguous fp32 [B, H, Nq] on q's device")
 
 
+def _check_mask(q_offset, left, right, sink):
+    return _int32("q_offset", q_offset), _int32("left", left), _int32("right", right), _int32("sink", sink)
+
+
 def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int = -1, right: int = 0,
                     sink: int = 0, q_offset: Optional[int] = None, scale: Optional[float] = None,
                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -591,14 +613,15 @@ def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int
     B, H, Hk, Nq, Nk, D = _check_window(q, k, v, out)
     _check_lse(lse, q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    q_offset, left, right, sink = _check_mask(Nk - Nq if q_offset is None else q_offset, left, right, sink)
     if out is None:
         out = torch.empty_like(q)
     if want_lse and lse is None:
         lse = q.new_empty((B, H, Nq), dtype=torch.float32)
     with _on(q):
         st = lib().dsa_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hk, Nq,
-                                       Nk, D, scale, Nk - Nq if q_offset is None else int(q_offset),
-                                       int(left), int(right), int(sink), out.data_ptr(), _ptr(lse), _stream(q))
+                                       Nk, D, scale, q_offset, left, right, sink, out.data_ptr(), _ptr(lse),
+                                       _stream(q))
     check(st, "dsa_window_attn_fwd")
     return out, lse
 
@@ -614,12 +637,13 @@ def window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
         raise ValueError("the forward's lse is required")
     _check_lse(lse, q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    q_offset = Nk - Nq if q_offset is None else int(q_offset)
-    dt, left, right, sink = _dtype_code(q), int(left), int(right), int(sink)
+    q_offset, left, right, sink = _check_mask(Nk - Nq if q_offset is None else q_offset, left, right, sink)
+    dt = _dtype_code(q)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
         n = int(lib().dsa_window_attn_bwd_workspace_size(dt, B, H, Hk, Nq, Nk, D, q_offset, left, right, sink))
         workspace = q.new_empty(max(n, 16), dtype=torch.uint8)
+    _check_workspace(workspace, q)
     with _on(q):
         st = lib().dsa_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                        dout.data_ptr(), lse.data_ptr(), dt, B, H, Hk, Nq, Nk, D, scale,
@@ -657,13 +681,16 @@ def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     st6 = _strides6(*([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k_cache, v_cache)))
     Hk, cap, dt = k_cache.shape[1], k_cache.shape[2], _dtype_code(q)
+    left, sink = _int32("left", left), _int32("sink", sink)
     if workspace is None:
-        n = int(lib().dsa_window_attn_decode_workspace_size(dt, B, H, Hk, Nq, cap, D, int(left), int(sink)))
+        n = int(lib().dsa_window_attn_decode_workspace_size(dt, B, H, Hk, Nq, cap, D, left, sink))
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+    if workspace is not None:
+        _check_workspace(workspace, q)
     with _on(q):
         st = lib().dsa_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), st6,
-                                          dt, B, H, Hk, Nq, cap, D, scale, lens.data_ptr(), int(left),
-                                          int(sink), out.data_ptr(), _ptr(lse), _ptr(workspace),
+                                          dt, B, H, Hk, Nq, cap, D, scale, lens.data_ptr(), left,
+                                          sink, out.data_ptr(), _ptr(lse), _ptr(workspace),
                                           0 if workspace is None else workspace.numel() * workspace.element_size(),
                                           _stream(q))
     check(st, "dsa_window_attn_decode")

@@ -565,7 +565,9 @@ dsa_status dsa_window_attn_fwd(const void* q, const void* k, const void* v, dsa_
  *
  *   out, lse   the forward's (lse is required);  dout  [B, H, Nq, D] in dt.
  *   dq         out, [B, H, Nq, D];  dk, dv  out, [B, Hk, Nk, D], in dt.  Keys
- *              that no query sees get 0, queries that see no key get dQ = 0.
+ *              that no query sees get 0, queries that see no key get dQ = 0
+ *              (a NaN or an infinity in q, k, v or dout reaches every gradient
+ *              of the tiles that load its row).
  *   workspace  >= dsa_window_attn_bwd_workspace_size(...) bytes, 16-byte
  *              aligned.
  * Every sum has a fixed order: two calls give the same bits.  bf16 runs on

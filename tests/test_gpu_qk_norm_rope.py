@@ -275,6 +275,18 @@ def test_position_past_the_table_is_reported():
     assert torch.equal(got[:, :, 2], ops.qk_norm_rope(xq, xk, wq, wk, plan.at(torch.full((N, 1), -1)))[0][:, :, 2])
 
 
+def test_positions_beyond_32_bits_are_reported():
+    N, D = 3, 64
+    xq, xk, wq, wk, _, _ = inputs(1, N, 2, 2, D, torch.bfloat16, seed=4)
+    plan = ops.RopePlan(torch.arange(N)[:, None], (D // 2,))
+    got = ops.qk_norm_rope(xq, xk, wq, wk, plan.at(torch.tensor([[0], [2**32 + 1], [-2**40]])))[0]
+    with pytest.raises(DSAError, match="rotation-position"):  # not taken for position 1
+        ops.device_status()
+    still = ops.qk_norm_rope(xq, xk, wq, wk, plan.at(torch.tensor([[0], [-1], [-1]])))[0]
+    ops.device_status()
+    assert torch.equal(got, still)
+
+
 def test_captured_and_other_stream():
     N, D = 64, 128
     xq, xk, wq, wk, dq, dk = inputs(1, N, 4, 4, D, torch.bfloat16, seed=2)

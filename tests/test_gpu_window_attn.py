@@ -316,6 +316,18 @@ def test_decode_bad_lengths_are_reported():
     assert torch.equal(out[1:2], ops.window_attn_decode(q[1:2], k[1:2], v[1:2], n[1:2]))
 
 
+def test_workspaces_elsewhere_are_refused():
+    q, k, v, do = make(1, 2, 1, 40, 40, 64, torch.bfloat16, seed=2)
+    out, lse = ops.window_attn_fwd(q, k, v, 8)
+    far = torch.empty(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        ops.window_attn_bwd(q, k, v, out, do, lse, 8, workspace=far)
+    with pytest.raises(ValueError, match="workspace"):
+        ops.window_attn_decode(q, k, v, torch.tensor([40], dtype=torch.int32, device="cuda"), 8, workspace=far)
+    with pytest.raises(ValueError, match="32 bits"):
+        ops.window_attn_fwd(q, k, v, 2**32)
+
+
 def test_decode_captured_over_a_growing_cache():
     q, k, v, _ = make(1, 8, 2, 1, 2048, 128, torch.bfloat16, seed=5)
     n = torch.tensor([1000], dtype=torch.int32, device="cuda")

@@ -194,3 +194,8 @@ def test_python_checks():
         window_layer._split(torch.zeros(1, 4, 7, 64), 4)
     with pytest.raises(ValueError, match="causal"):
         window_layer.Stream(1, 2, 2, 8, 64, type("P", (), {"table": x}), window_layer.Mask(1, 1, 0))
+    with pytest.raises(ValueError, match="CUDA device"):
+        ops.rope_table(8, 4, device="cpu")
+    for v in (2**31, -2**31 - 1):                           # not cut to 32 bits
+        with pytest.raises(ValueError, match="32 bits"):
+            ops._check_mask(0, v, 0, 0)
