@@ -28,9 +28,12 @@ def _stream(t: torch.Tensor):
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(t: torch.Tensor):
     """t's device as the current one."""
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE if t.device.index == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -340,32 +343,30 @@ def pack8(x: torch.Tensor) -> Act8:
     amax / 127 for each row, half-even rounding."""
     if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
         raise ValueError("x must be a contiguous CUDA tensor [..., D]")
-    dt, D = _dtype_code(x), x.shape[-1]
-    a = Act8(torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32))
-    if x.numel() == 0:
-        return a
-    with _on(x):
-        st = lib().dsa_pack8(x.data_ptr(), dt, x.numel() // D, D, a.codes.data_ptr(),
-                             a.scales.data_ptr(), _stream(x))
-    check(st, "dsa_pack8")
-    return a
+    dt, shape, n = _dtype_code(x), x.shape, x.numel()
+    D = shape[-1]
+    codes, scales = x.new_empty(shape, dtype=torch.int8), x.new_empty(shape[:-1], dtype=torch.float32)
+    if n > 0:
+        with _on(x):
+            st = lib().dsa_pack8(x.data_ptr(), dt, n // D, D, codes.data_ptr(), scales.data_ptr(), _stream(x))
+        check(st, "dsa_pack8")
+    return Act8(codes, scales)
 
 
 def unpack8(a: Act8, dtype: torch.dtype = torch.bfloat16,
             out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values that 8-bit rows stand for, as bf16 or fp32."""
     _check_act8(a)
+    codes, scales = a
     if out is None:
-        out = torch.empty_like(a.codes, dtype=dtype)
-    elif out.shape != a.codes.shape or out.device != a.codes.device or not out.is_contiguous():
+        out = codes.new_empty(codes.shape, dtype=dtype)
+    elif out.shape != codes.shape or out.device != codes.device or not out.is_contiguous():
         raise ValueError("out must be contiguous, of the codes' shape and device")
-    dt, D = _dtype_code(out), out.shape[-1]
-    if out.numel() == 0:
-        return out
-    with _on(out):
-        st = lib().dsa_unpack8(a.codes.data_ptr(), a.scales.data_ptr(), dt, out.numel() // D, D,
-                               out.data_ptr(), _stream(out))
-    check(st, "dsa_unpack8")
+    dt, n, D = _dtype_code(out), codes.numel(), codes.shape[-1]
+    if n > 0:
+        with _on(out):
+            st = lib().dsa_unpack8(codes.data_ptr(), scales.data_ptr(), dt, n // D, D, out.data_ptr(), _stream(out))
+        check(st, "dsa_unpack8")
     return out
 
 
@@ -461,13 +462,21 @@ class RopePlan:
 
 def _token_rows(x: torch.Tensor, what: str):
     """Strides of b, n, h of token-major rows [B, N, H, D], D contiguous."""
-    if x.dim() != 4 or not x.is_cuda or (x.shape[-1] > 1 and x.stride(-1) != 1):
+    n, st = x.shape, x.stride()
+    if len(n) != 4 or not x.is_cuda or (n[3] > 1 and st[3] != 1):
         raise ValueError(f"{what} must be a CUDA tensor [B, N, H, D] with contiguous rows")
-    return [x.stride(i) if x.shape[i] > 1 else 0 for i in range(3)]
+    return _strides3(n, st)
+
+
+def _strides3(n, st):
+    return st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0
+
+
+_Int64x6 = ctypes.c_int64 * 6
 
 
 def _strides6(a, b):
-    return (ctypes.c_int64 * 6)(*a, *b)
+    return _Int64x6(*a, *b)
 
 
 def _check_norm_rope(xq, xk, wq, wk, plan: RopePlan):
@@ -679,7 +688,7 @@ def window_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         raise ValueError("out must match q")
     _check_lse(lse, q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    st6 = _strides6(*([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k_cache, v_cache)))
+    st6 = _strides6(*(_strides3(t.shape, t.stride()) for t in (k_cache, v_cache)))
     Hk, cap, dt = k_cache.shape[1], k_cache.shape[2], _dtype_code(q)
     left, sink = _int32("left", left), _int32("sink", sink)
     if workspace is None:
