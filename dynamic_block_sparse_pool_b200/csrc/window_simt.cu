@@ -13,7 +13,12 @@
 // atomics: equal bits from run to run.  A tile pair takes about 5 us, so where
 // the tiles of one side are few, or one of them (a sink's) sees far more than
 // the others, a gradient tile's pairs are cut into chunks (SimtChunks), one CTA
-// each, whose partial sums a last kernel adds in order.
+// each, whose partial sums a last kernel adds in order.  All gradients come out
+// of one launch, so dQ's CTAs fill in where dK's and dV's run out (1,003 tokens,
+// 4 heads on 2, D = 64: 101 -> 81 us with the row terms and the join; 2 x 4,000
+// tokens, 8 heads on 4, D = 128, causal over 1,000: 3.56 -> 3.28 ms, 22 TFLOP/s).
+// Forward of the latter 0.98 ms, 29 TFLOP/s.  Shared-memory reads are at 62 % of
+// their peak rate and FMA at 50 %, with 8 warps on an SM (D = 128).
 #include <algorithm>
 
 #include "window_attn.cuh"
@@ -219,27 +224,52 @@ __device__ __forceinline__ void stage_vec(float* dst, const float* src, int r0, 
   if (threadIdx.x < T) dst[threadIdx.x] = r0 + threadIdx.x < end ? src[r0 + threadIdx.x] : pad;
 }
 
+struct BwdSimt {
+  const float *q, *k, *v, *dout, *lse, *delta;
+  Window w;
+  int heads_q, heads_k, group;  // B H, B Hk, H / Hk
+  float scale;
+  SimtChunks cut;
+  float *dq, *dk, *dv;          // gradients, or the chunks' shares of them
+  unsigned ctas_k;              // CTAs of dK and dV; the others are dQ's
+};
+
+// Chunk y of the pairs of tile x of all tiles of a gradient: the first chunks of
+// all tiles come first.
+struct Place {
+  int head, tile, y;
+  __device__ __forceinline__ Place(unsigned i, int heads, int tiles) {
+    const unsigned all = (unsigned)heads * tiles, x = i % all;
+    y = (int)(i / all);
+    head = (int)(x / tiles);
+    tile = (int)(x - head * tiles);
+  }
+};
+
 // dQ of a query tile
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
-window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                      const float* __restrict__ dout, const float* __restrict__ lse, const float* __restrict__ delta,
-                      const Window w, int group, float scale, int chunk, float* __restrict__ dq) {
+__device__ __forceinline__ void dq_tile(const BwdSimt& a, unsigned i) {
+  const float* __restrict__ q = a.q;
+  const float* __restrict__ k = a.k;
+  const float* __restrict__ v = a.v;
+  const float* __restrict__ dout = a.dout;
+  const Window w = a.w;
+  const float scale = a.scale;
   constexpr int P = padded<D>();
   extern __shared__ __align__(16) float sm[];
   float *Q = sm, *O = Q + T * P, *K = O + T * P, *V = K + T * P, *W = V + T * P, *ls = W + T * SP, *de = ls + T;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int tiles = ceil_div(w.Nq, T), bh = blockIdx.x / tiles, q0 = (blockIdx.x - bh * tiles) * T;
-  const int q1 = min(q0 + T, w.Nq);
-  const size_t qh = (size_t)bh * w.Nq * D, kh = (size_t)(bh / group) * w.Nk * D;
+  const Place at(i, a.heads_q, ceil_div(w.Nq, T));
+  const int bh = at.head, q0 = at.tile * T, q1 = min(q0 + T, w.Nq);
+  const size_t qh = (size_t)bh * w.Nq * D, kh = (size_t)(bh / a.group) * w.Nk * D;
   const KeyTiles<T> kt = KeyTiles<T>::of(w, q0, q1);
-  const int e0 = blockIdx.y * chunk, e1 = min(kt.count(), e0 + chunk);
-  if (blockIdx.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
-  dq += blockIdx.y * ((size_t)(gridDim.x / tiles) * w.Nq * D);
+  const int e0 = at.y * a.cut.chunk_q, e1 = min(kt.count(), e0 + a.cut.chunk_q);
+  if (at.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
+  float* dq = a.dq + at.y * ((size_t)a.heads_q * w.Nq * D);
   stage<D>(Q, q + qh, q0, w.Nq);
   stage<D>(O, dout + qh, q0, w.Nq);
-  stage_vec(ls, lse + (size_t)bh * w.Nq, q0, w.Nq, -INFINITY);
-  stage_vec(de, delta + (size_t)bh * w.Nq, q0, w.Nq, 0.f);
+  stage_vec(ls, a.lse + (size_t)bh * w.Nq, q0, w.Nq, -INFINITY);
+  stage_vec(de, a.delta + (size_t)bh * w.Nq, q0, w.Nq, 0.f);
   float acc[4][D / 16] = {};
   for (int e = e0; e < e1; ++e) {
     const int k0 = kt.tile(e) * T;
@@ -252,9 +282,9 @@ window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, 
     product_nt<D>(dp, O, V, ty, tx);
     weights(s, dp, p, ds, w, q0, k0, all_visible(w, q0, q1, k0, k0 + T), scale, ls, de, ty, tx);
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) W[(ty + 16 * a) * SP + tx + 16 * b] = ds[a][b];
+      for (int b = 0; b < 4; ++b) W[(ty + 16 * c) * SP + tx + 16 * b] = ds[c][b];
     __syncthreads();
     product_nn<D>(acc, W, K, ty, tx);
   }
@@ -264,25 +294,26 @@ window_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, 
 
 // dK and dV of a key tile, over the query heads of its key head
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
-window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                        const float* __restrict__ dout, const float* __restrict__ lse,
-                        const float* __restrict__ delta, const Window w, int group, float scale, int chunk,
-                        float* __restrict__ dk, float* __restrict__ dv) {
+__device__ __forceinline__ void dkdv_tile(const BwdSimt& a, unsigned i) {
+  const float* __restrict__ q = a.q;
+  const float* __restrict__ dout = a.dout;
+  const Window w = a.w;
+  const int group = a.group;
+  const float scale = a.scale;
   constexpr int P = padded<D>();
   extern __shared__ __align__(16) float sm[];
   float *K = sm, *V = K + T * P, *Q = V + T * P, *O = Q + T * P, *W = O + T * P, *ls = W + T * SP, *de = ls + T;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int tiles = ceil_div(w.Nk, T), kv = blockIdx.x / tiles, k0 = (blockIdx.x - kv * tiles) * T;
-  const int k1 = min(k0 + T, w.Nk);
+  const Place at(i, a.heads_k, ceil_div(w.Nk, T));
+  const int kv = at.head, k0 = at.tile * T, k1 = min(k0 + T, w.Nk);
   const size_t kh = (size_t)kv * w.Nk * D;
   const QueryRun run = QueryRun::of(w, k0, k1);
   const int i0 = run.q0 / T, per = run.tiles<T>(), n = per * group;  // query tiles per head, head after head
-  const int e0 = blockIdx.y * chunk, e1 = min(n, e0 + chunk);
-  if (blockIdx.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
-  const size_t share = blockIdx.y * ((size_t)(gridDim.x / tiles) * w.Nk * D);
-  stage<D>(K, k + kh, k0, w.Nk);
-  stage<D>(V, v + kh, k0, w.Nk);
+  const int e0 = at.y * a.cut.chunk_k, e1 = min(n, e0 + a.cut.chunk_k);
+  if (at.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
+  const size_t share = at.y * ((size_t)a.heads_k * w.Nk * D);
+  stage<D>(K, a.k + kh, k0, w.Nk);
+  stage<D>(V, a.v + kh, k0, w.Nk);
   float ak[4][D / 16] = {}, av[4][D / 16] = {};
   for (int e = e0; e < e1; ++e) {
     const int h = e / per, q0 = (i0 + e - h * per) * T;
@@ -290,8 +321,8 @@ window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k
     __syncthreads();
     stage<D>(Q, q + qh, q0, w.Nq);
     stage<D>(O, dout + qh, q0, w.Nq);
-    stage_vec(ls, lse + bh * w.Nq, q0, w.Nq, -INFINITY);
-    stage_vec(de, delta + bh * w.Nq, q0, w.Nq, 0.f);
+    stage_vec(ls, a.lse + bh * w.Nq, q0, w.Nq, -INFINITY);
+    stage_vec(de, a.delta + bh * w.Nq, q0, w.Nq, 0.f);
     __syncthreads();
     float s[4][4] = {}, dp[4][4] = {}, p[4][4], ds[4][4];
     product_nt<D>(s, Q, K, ty, tx);
@@ -299,44 +330,65 @@ window_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k
     weights(s, dp, p, ds, w, q0, k0, all_visible(w, q0, min(q0 + T, w.Nq), k0, k0 + T), scale, ls, de, ty, tx);
     // transposed into shared memory: row = key
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = p[a][b];
+      for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * c] = p[c][b];
     __syncthreads();
     product_nn<D>(av, W, O, ty, tx);
     __syncthreads();
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * a] = ds[a][b];
+      for (int b = 0; b < 4; ++b) W[(tx + 16 * b) * SP + ty + 16 * c] = ds[c][b];
     __syncthreads();
     product_nn<D>(ak, W, Q, ty, tx);
   }
   float one[4] = {1.f, 1.f, 1.f, 1.f}, mul[4] = {scale, scale, scale, scale};
-  store_rows<D>(dv + share + kh, av, k0, k1, one, ty, tx);
-  store_rows<D>(dk + share + kh, ak, k0, k1, mul, ty, tx);
+  store_rows<D>(a.dv + share + kh, av, k0, k1, one, ty, tx);
+  store_rows<D>(a.dk + share + kh, ak, k0, k1, mul, ty, tx);
+}
+
+// All gradients: dK's and dV's CTAs, then dQ's, which fill in behind them.
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
+window_bwd_simt_kernel(const BwdSimt a) {
+  if (blockIdx.x < a.ctas_k)
+    dkdv_tile<D>(a, blockIdx.x);
+  else
+    dq_tile<D>(a, blockIdx.x - a.ctas_k);
 }
 
 // Sums the chunks' shares of one gradient, [chunks][heads][N][D] -> [heads][N][D];
 // a row of a tile has as many shares as the tile has chunks (at least one).
+// Thread i: four columns of a row.
 template <int D, bool KEYS>
-__global__ void __launch_bounds__(kThreads)
-window_join_simt_kernel(const float* __restrict__ part, const Window w, int group, int chunk, long long rows,
-                        float* __restrict__ out) {
-  constexpr int V = D / 4;
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, row = i / V;
-  if (row >= rows) return;
+__device__ __forceinline__ void join(const BwdSimt& a, const float* __restrict__ part, long long rows, long long i,
+                                     float* __restrict__ out) {
+  const long long row = i / (D / 4);
+  const Window w = a.w;
   const int N = KEYS ? w.Nk : w.Nq, x0 = (int)(row % N) / T * T, x1 = min(x0 + T, N);
-  const int n = KEYS ? QueryRun::of(w, x0, x1).tiles<T>() * group : KeyTiles<T>::of(w, x0, x1).count();
-  const int chunks = max(1, ceil_div(n, chunk));
+  const int n = KEYS ? QueryRun::of(w, x0, x1).tiles<T>() * a.group : KeyTiles<T>::of(w, x0, x1).count();
+  const int chunks = max(1, ceil_div(n, KEYS ? a.cut.chunk_k : a.cut.chunk_q));
   const float4* p = reinterpret_cast<const float4*>(part) + i;
   float4 s = *p;
+#pragma unroll 4
   for (int c = 1; c < chunks; ++c) {
-    p += rows * V;
+    p += rows * (D / 4);
     const float4 x = *p;
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
   reinterpret_cast<float4*>(out)[i] = s;
+}
+
+// The gradients that have shares: rows_k of dK and of dV, rows_q of dQ (0: none).
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+window_join_simt_kernel(const BwdSimt a, long long rows_k, long long rows_q, float* dk, float* dv, float* dq) {
+  constexpr int V = D / 4;
+  long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (i < rows_k * V) return join<D, true>(a, a.dk, rows_k, i, dk);
+  if ((i -= rows_k * V) < rows_k * V) return join<D, true>(a, a.dv, rows_k, i, dv);
+  if ((i -= rows_k * V) < rows_q * V) join<D, false>(a, a.dq, rows_q, i, dq);
 }
 
 template <int D>
@@ -353,31 +405,36 @@ cudaError_t fwd_d(const WindowAttn& a, cudaStream_t s) {
 template <int D>
 cudaError_t bwd_d(const WindowAttn& a, cudaStream_t s) {
   const size_t smem = (4 * T * padded<D>() + T * SP + 2 * T) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(window_dq_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(window_bwd_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(window_dkdv_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const float *q = static_cast<const float*>(a.q), *k = static_cast<const float*>(a.k),
-              *v = static_cast<const float*>(a.v), *g = static_cast<const float*>(a.dout);
-  const int group = a.H / a.Hk;
-  const SimtChunks c = simt_chunks(a.B, a.H, a.Hk, a.w);
-  const long long rq = (long long)a.B * a.H * a.w.Nq, rk = (long long)a.B * a.Hk * a.w.Nk;
+  float *dq = static_cast<float*>(a.dq), *dk = static_cast<float*>(a.dk), *dv = static_cast<float*>(a.dv);
+  BwdSimt p;
+  p.q = static_cast<const float*>(a.q);
+  p.k = static_cast<const float*>(a.k);
+  p.v = static_cast<const float*>(a.v);
+  p.dout = static_cast<const float*>(a.dout);
+  p.lse = a.lse;
+  p.delta = a.delta;
+  p.w = a.w;
+  p.heads_q = a.B * a.H;
+  p.heads_k = a.B * a.Hk;
+  p.group = a.H / a.Hk;
+  p.scale = a.scale;
+  p.cut = simt_chunks(a.B, a.H, a.Hk, a.w);
+  const long long rq = (long long)p.heads_q * a.w.Nq, rk = (long long)p.heads_k * a.w.Nk;
+  const bool cut_q = p.cut.chunks_q > 1, cut_k = p.cut.chunks_k > 1;
   // shares: dQ's, dK's, dV's, each where it has more than one
-  float* pq = c.chunks_q > 1 ? a.shares : static_cast<float*>(a.dq);
-  float* pk = c.chunks_k > 1 ? a.shares + (c.chunks_q > 1 ? c.chunks_q * rq * D : 0) : static_cast<float*>(a.dk);
-  float* pv = c.chunks_k > 1 ? pk + c.chunks_k * rk * D : static_cast<float*>(a.dv);
-  window_dq_simt_kernel<D><<<dim3((unsigned)(a.B * a.H * ceil_div(a.w.Nq, T)), (unsigned)c.chunks_q), kThreads, smem, s>>>(
-      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, c.chunk_q, pq);
+  p.dq = cut_q ? a.shares : dq;
+  p.dk = cut_k ? a.shares + (cut_q ? p.cut.chunks_q * rq * D : 0) : dk;
+  p.dv = cut_k ? p.dk + p.cut.chunks_k * rk * D : dv;
+  p.ctas_k = (unsigned)(p.heads_k * ceil_div(a.w.Nk, T)) * p.cut.chunks_k;
+  const unsigned ctas_q = (unsigned)(p.heads_q * ceil_div(a.w.Nq, T)) * p.cut.chunks_q;
+  window_bwd_simt_kernel<D><<<p.ctas_k + ctas_q, kThreads, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  window_dkdv_simt_kernel<D><<<dim3((unsigned)(a.B * a.Hk * ceil_div(a.w.Nk, T)), (unsigned)c.chunks_k), kThreads, smem, s>>>(
-      q, k, v, g, a.lse, a.delta, a.w, group, a.scale, c.chunk_k, pk, pv);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  auto grid = [](long long rows) { return (unsigned)((rows * (D / 4) + kThreads - 1) / kThreads); };
-  if (c.chunks_q > 1)
-    window_join_simt_kernel<D, false><<<grid(rq), kThreads, 0, s>>>(pq, a.w, group, c.chunk_q, rq, static_cast<float*>(a.dq));
-  if (c.chunks_k > 1) {
-    window_join_simt_kernel<D, true><<<grid(rk), kThreads, 0, s>>>(pk, a.w, group, c.chunk_k, rk, static_cast<float*>(a.dk));
-    window_join_simt_kernel<D, true><<<grid(rk), kThreads, 0, s>>>(pv, a.w, group, c.chunk_k, rk, static_cast<float*>(a.dv));
+  if (cut_q || cut_k) {
+    const long long rows = (cut_k ? 2 * rk : 0) + (cut_q ? rq : 0);
+    window_join_simt_kernel<D><<<(unsigned)((rows * (D / 4) + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+        p, cut_k ? rk : 0, cut_q ? rq : 0, dk, dv, dq);
   }
   return cudaGetLastError();
 }
