@@ -5,12 +5,13 @@
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
 // dK and dV summed over the query heads that share the key head.
 //
-// Two kernels, one CTA per tile of 128 rows:
+// One CTA per tile of 128 rows:
 //   dq    one query tile against the key tiles it sees;
 //   dkdv  one key tile against the query tiles that see it, for each query
 //         head of its group in turn: every sum has a fixed order, no atomics.
 //         A tile that many more queries see than the others (one with sinks) is
 //         cut into several CTAs, whose fp32 shares window_join adds in order.
+// Both kinds are CTAs of one launch.
 // Per tile pair the S-type products go to tensor memory as fp32, the
 // element-wise pass writes packed bf16 terms back into S's columns, and the
 // gradient products take them from there.  For dQ, dS goes in as two terms,
@@ -35,15 +36,15 @@
 // error word and the CTA winds down.
 //
 // Measured, 17,776 tokens, 8 heads, D = 64, every token in sight of 5,400 others
-// and a prefix of 226: dQ 430 us (511 with one buffer of S), dK/dV 470 (617);
-// exp2 keeps its unit and the MMAs the tensor cores (N = 64 costs them as much
-// as N = 128) half of the time each, and the two do not overlap in full.  A
-// delay of half the warps by a third of a pass, so that one half computes while
-// the other reads, costs 5 %.  48 heads: 4.8 ms in all (590 TFLOP/s).
-// 8,192 tokens, 16 query heads on 4, D = 128, causal over 2,048, four sinks: dQ
-// 229 us, dK/dV 270 (357 with the sinks' tile uncut and last, 376 with dP ahead
-// of the gradients), 0.52 ms in all (575 TFLOP/s); causal without a window
-// 1.03 ms (667).
+// and a prefix of 226, each kind alone: dq 430 us (511 with one buffer of S), dkdv
+// 470 (617); exp2 keeps its unit and the MMAs the tensor cores (N = 64 costs them
+// as much as N = 128) half of the time each, and the two do not overlap in full.
+// A delay of half the warps by a third of a pass, so that one half computes while
+// the other reads, costs 5 %.  48 heads: 4.9 ms in all (575 TFLOP/s).
+// 8,192 tokens, 16 query heads on 4, D = 128, causal over 2,048, four sinks: dq
+// 229 us, dkdv 270 (357 with the sinks' tile uncut and last, 376 with dP ahead
+// of the gradients), 0.47 ms in all (640 TFLOP/s); causal without a window
+// 0.82 ms (840).
 #include <algorithm>
 
 #include "bwd_tiles.cuh"
@@ -57,11 +58,12 @@ using namespace bwd;
 
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-// warps 10 and 11 only fill up the third warpgroup: of its registers (168 a thread
-// at launch) the element-wise warps take what it does not need
-// (2 % at D = 64, where dK/dV else spills)
-constexpr int kElementRegs = 208, kOtherRegs = 88;
-static_assert(256 * kElementRegs + 128 * kOtherRegs <= 168 * kThreads);
+// Warps 10 and 11 only fill up the third warpgroup: of its registers (168 a thread
+// at launch) the element-wise warps take what it does not need.
+template <int D> constexpr int kElementRegs = D == 64 ? 216 : 208;  // (208 at D = 64: 3 % slower, 216 at 128: 2 %)
+template <int D> constexpr int kOtherRegs = D == 64 ? 72 : 88;
+static_assert(256 * kElementRegs<64> + 128 * kOtherRegs<64> <= 168 * kThreads);
+static_assert(256 * kElementRegs<128> + 128 * kOtherRegs<128> <= 168 * kThreads);
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -100,11 +102,12 @@ struct BwdParams {
   BwdChunks cut;   // dkdv
   float* shares;   // dkdv: [slot][dV, dK][128][D]
   int group;       // query heads per key head
-  int tiles;       // tiles per head of the CTA's side
+  int tiles_q, tiles_k;  // tiles per head
   float scale, scale_log2;
   const float *lse, *delta;
-  int heads;       // dq: B H
+  int heads;       // B H
   bool by_tile;    // dq: order_by_tile
+  unsigned ctas_k; // CTAs of dkdv; the others are dq's
 };
 
 // bits 0 .. v-1
@@ -329,23 +332,21 @@ __device__ __forceinline__ void issue_mmas(const Cta& c, int n, Grads grads, uns
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const BwdParams p,
-                 __nv_bfloat16* __restrict__ dq, unsigned* err) {
+__device__ __forceinline__ void dq_tile(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                        const CUtensorMap& tmO, const BwdParams& p, unsigned block, uint8_t* smem,
+                                        __nv_bfloat16* __restrict__ dq, unsigned* err) {
   using L = Layout<D, 1>;
-  extern __shared__ __align__(1024) uint8_t smem[];
   Cta c;
   if (!cta_begin<L>(c, smem, err)) return;
-  const int run = p.by_tile ? p.heads : p.tiles, o = blockIdx.x / run, r = blockIdx.x - o * run;
-  const int bh = p.by_tile ? r : o, q0 = (p.tiles - 1 - (p.by_tile ? o : r)) * BB;
+  const int run = p.by_tile ? p.heads : p.tiles_q, o = block / run, r = block - o * run;
+  const int bh = p.by_tile ? r : o, q0 = (p.tiles_q - 1 - (p.by_tile ? o : r)) * BB;
   const int q1 = min(q0 + BB, p.w.Nq);
   const KeyTiles<BB> kt = KeyTiles<BB>::of(p.w, q0, q1);
   const int n = kt.count();
   int issued_a = 0, issued_b = 0;
 
   if (c.warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
     if (c.warp == kLoadWarp) {
       if (c.lane == 0 && n > 0)
         load_tiles<D, L>(c, &tmQ, &tmO, q0, bh, &tmK, &tmV, n, [&](int it, int& head, int& row) {
@@ -362,7 +363,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElementRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElementRegs<D>));
     const int h = c.warp >> 2, row = 32 * (c.warp & 3) + c.lane;
     const uint32_t lanes = (uint32_t)(32 * (c.warp & 3)) << 16;
     const bool valid = q0 + row < q1;
@@ -439,27 +440,26 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const BwdParams p,
-                   __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, unsigned* err) {
+__device__ __forceinline__ void dkdv_tile(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                          const CUtensorMap& tmO, const BwdParams& p, unsigned block, uint8_t* smem,
+                                          __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+                                          unsigned* err) {
   using L = Layout<D, 2>;
   constexpr uint32_t kColV = L::kColG, kColK = L::kColG + D;
   int kv, tile, part;
-  p.cut.place(blockIdx.x, p.tiles, kv, tile, part);
+  p.cut.place(block, p.tiles_k, kv, tile, part);
   const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
   const QueryRun run = QueryRun::of(p.w, k0, k1);
   const int i0 = run.q0 / BB, per = run.tiles<BB>();
   // pairs e0 .. e0 + n - 1 of the tile: query tiles per head, head after head
   const int e0 = part * p.cut.chunk(tile), n = min(per * p.group - e0, p.cut.chunk(tile));
   if (part > 0 && n <= 0) return;  // (part 0 writes its zeros)
-  extern __shared__ __align__(1024) uint8_t smem[];
   Cta c;
   if (!cta_begin<L>(c, smem, err)) return;
   int issued_a = 0, issued_b = 0;
 
   if (c.warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
     if (c.warp == kLoadWarp) {
       if (c.lane == 0 && n > 0)
         load_tiles<D, L>(c, &tmK, &tmV, k0, kv, &tmQ, &tmO, n, [&](int it, int& head, int& row) {
@@ -479,7 +479,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElementRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElementRegs<D>));
     // thread = key row; columns = the query tile's queries, half h of them
     const int h = c.warp >> 2, row = 32 * (c.warp & 3) + c.lane, wt = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (c.warp & 3)) << 16;
@@ -577,7 +577,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         if (p.cut.parts(tile) > 1) {  // this CTA's share, for window_join_kernel
           float4* sh = reinterpret_cast<float4*>(
-              p.shares + ((p.cut.slot(kv, p.tiles, tile, part) * 2 + h) * BB + row) * D + 32 * g32);
+              p.shares + ((p.cut.slot(kv, p.tiles_k, tile, part) * 2 + h) * BB + row) * D + 32 * g32);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             sh[x] = make_float4(__uint_as_float(g[4 * x]), __uint_as_float(g[4 * x + 1]), __uint_as_float(g[4 * x + 2]),
@@ -591,6 +591,23 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   cta_end<L>(c, n, issued_a, issued_b);
 }
 
+// dkdv's CTAs, then dq's, which fill in where those run out: 1,003 tokens, 4
+// heads on 2, D = 64: 44 -> 32 us, 8,192 tokens, 16 heads on 4, D = 128, causal:
+// 1,020 -> 815 us.  (At D = 64 the compiler spills a little more for having both:
+// 1 % slower than two launches where there are dozens of waves of CTAs.)
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const BwdParams p,
+                  __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+                  unsigned* err) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (blockIdx.x < p.ctas_k)
+    dkdv_tile<D>(tmQ, tmK, tmV, tmO, p, blockIdx.x, smem, dk, dv, err);
+  else
+    dq_tile<D>(tmQ, tmK, tmV, tmO, p, blockIdx.x - p.ctas_k, smem, dq, err);
+}
+
 // dK and dV of the tiles that several CTAs share, summed in order: four columns
 // of a row per thread.  Grid: x = heads * tiles that are cut, y = kJoinCtas<D>.
 template <int D>
@@ -599,7 +616,7 @@ constexpr int kJoinCtas = 2 * BB * (D / 4) / 256;
 template <int D>
 __global__ void __launch_bounds__(256)
 window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
-  const int cut = p.cut.cut_tiles(p.tiles), kv = blockIdx.x / cut, tile = p.cut.cut_tile(blockIdx.x - kv * cut);
+  const int cut = p.cut.cut_tiles(p.tiles_k), kv = blockIdx.x / cut, tile = p.cut.cut_tile(blockIdx.x - kv * cut);
   const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
   const int n = QueryRun::of(p.w, k0, k1).tiles<BB>() * p.group, parts = max(1, ceil_div(n, p.cut.chunk(tile)));
   const int i = blockIdx.y * 256 + threadIdx.x, h = i / (BB * (D / 4)), r = i / (D / 4) % BB, d = 4 * (i % (D / 4));
@@ -608,7 +625,7 @@ window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloa
 #pragma unroll 4
   for (int c = 0; c < parts; ++c) {
     const float4 x =
-        *reinterpret_cast<const float4*>(p.shares + ((p.cut.slot(kv, p.tiles, tile, c) * 2 + h) * BB + r) * D + d);
+        *reinterpret_cast<const float4*>(p.shares + ((p.cut.slot(kv, p.tiles_k, tile, c) * 2 + h) * BB + r) * D + d);
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
   const float mul = h ? p.scale : 1.f;
@@ -621,24 +638,30 @@ window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloa
 template <int D>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                      const WindowAttn& a, cudaStream_t s) {
-  const int smem_q = Layout<D, 1>::kBytes, smem_kv = Layout<D, 2>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
+  const int smem = std::max(Layout<D, 1>::kBytes, Layout<D, 2>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(window_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(window_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
-  if (e != cudaSuccess) return e;
-  BwdParams p{a.w,    bwd_chunks(a.B, a.H, a.Hk, a.w), a.shares, a.H / a.Hk, ceil_div(a.w.Nq, BB),
-              a.scale, a.scale * kLog2e,                a.lse,    a.delta,   a.B * a.H,
-              order_by_tile(a)};
-  window_dq_kernel<D><<<a.B * a.H * p.tiles, kThreads, smem_q, s>>>(mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dq),
-                                                                  a.err);
+  BwdParams p;
+  p.w = a.w;
+  p.cut = bwd_chunks(a.B, a.H, a.Hk, a.w);
+  p.shares = a.shares;
+  p.group = a.H / a.Hk;
+  p.tiles_q = ceil_div(a.w.Nq, BB);
+  p.tiles_k = ceil_div(a.w.Nk, BB);
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * kLog2e;
+  p.lse = a.lse;
+  p.delta = a.delta;
+  p.heads = a.B * a.H;
+  p.by_tile = order_by_tile(a);
+  p.ctas_k = (unsigned)p.cut.ctas(p.tiles_k);
+  auto *dq = static_cast<__nv_bfloat16*>(a.dq), *dk = static_cast<__nv_bfloat16*>(a.dk),
+       *dv = static_cast<__nv_bfloat16*>(a.dv);
+  window_bwd_kernel<D><<<p.ctas_k + (unsigned)(p.heads * p.tiles_q), kThreads, smem, s>>>(mq, mk, mv, mo, p, dq, dk, dv,
+                                                                                        a.err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  p.tiles = ceil_div(a.w.Nk, BB);
-  window_dkdv_kernel<D><<<p.cut.ctas(p.tiles), kThreads, smem_kv, s>>>(
-      mq, mk, mv, mo, p, static_cast<__nv_bfloat16*>(a.dk), static_cast<__nv_bfloat16*>(a.dv), a.err);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (const int cut = p.cut.cut_tiles(p.tiles))
-    window_join_kernel<D><<<dim3(a.B * a.Hk * cut, kJoinCtas<D>), 256, 0, s>>>(
-        p, static_cast<__nv_bfloat16*>(a.dk), static_cast<__nv_bfloat16*>(a.dv));
+  if (const int cut = p.cut.cut_tiles(p.tiles_k))
+    window_join_kernel<D><<<dim3(a.B * a.Hk * cut, kJoinCtas<D>), 256, 0, s>>>(p, dk, dv);
   return cudaGetLastError();
 }
 
