@@ -77,6 +77,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256)
 delta_kernel(const T* __restrict__ out, const T* __restrict__ dout, long long rows,
              float* __restrict__ delta) {
+  let_next_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long r = (long long)blockIdx.x * 8 + warp;
   if (r >= rows) return;

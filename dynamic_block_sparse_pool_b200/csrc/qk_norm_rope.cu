@@ -297,6 +297,7 @@ qk_norm_rope_bwd_kernel(const BwdArgs<TX, TG> a) {
   constexpr int TPR = D / 8, RPW = 32 / TPR, SX = Slots<TX>::kCount, SLOTS = bwd_slots<TX, TG>();
   extern __shared__ __align__(16) uint4 ring[];  // [kDepth][SLOTS][kThreads]
   __shared__ float red[kWarps * RPW][D];
+  let_next_start();
   const int lane = threadIdx.x & 31, sub = lane % TPR, slot = lane / TPR, warp = threadIdx.x >> 5;
   const bool is_k = blockIdx.y >= a.parts_q;
   const BwdSide<TX, TG>& side = is_k ? a.k : a.q;
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(1024)
 weight_grad_kernel(const float* __restrict__ part, int ctas_q, int ctas_k, int D, float* __restrict__ dwq,
                    float* __restrict__ dwk) {
   __shared__ float red[1024];
+  wait_for_previous();
   const float* p0 = blockIdx.x ? part + (long long)ctas_q * D : part;
   const int ctas = blockIdx.x ? ctas_k : ctas_q, col = threadIdx.x % D, p = threadIdx.x / D, parts = 1024 / D;
   float sum = 0.f;
@@ -532,8 +534,7 @@ cudaError_t bwd_t(const NormRopeBwd& f, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   qk_norm_rope_bwd_kernel<TX, TG, D, HALVES><<<dim3(g.x, g.parts_q + g.parts_k), kThreads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  weight_grad_kernel<<<2, 1024, 0, s>>>(f.part, g.x * g.parts_q, g.x * g.parts_k, D, f.dwq, f.dwk);
-  return cudaGetLastError();
+  return launch_next(weight_grad_kernel, 2, 1024, 0, s, f.part, g.x * g.parts_q, g.x * g.parts_k, D, f.dwq, f.dwk);
 }
 
 template <typename TX, typename TG>

@@ -338,6 +338,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tmQ, const CUtensorMa
   using L = Layout<D, 1>;
   Cta c;
   if (!cta_begin<L>(c, smem, err)) return;
+  wait_for_previous();
   const int run = p.by_tile ? p.heads : p.tiles_q, o = block / run, r = block - o * run;
   const int bh = p.by_tile ? r : o, q0 = (p.tiles_q - 1 - (p.by_tile ? o : r)) * BB;
   const int q1 = min(q0 + BB, p.w.Nq);
@@ -456,6 +457,7 @@ __device__ __forceinline__ void dkdv_tile(const CUtensorMap& tmQ, const CUtensor
   if (part > 0 && n <= 0) return;  // (part 0 writes its zeros)
   Cta c;
   if (!cta_begin<L>(c, smem, err)) return;
+  wait_for_previous();
   int issued_a = 0, issued_b = 0;
 
   if (c.warp >= kMmaWarp) {
@@ -602,6 +604,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                   __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
                   unsigned* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  let_next_start();
   if (blockIdx.x < p.ctas_k)
     dkdv_tile<D>(tmQ, tmK, tmV, tmO, p, blockIdx.x, smem, dk, dv, err);
   else
@@ -616,6 +619,7 @@ constexpr int kJoinCtas = 2 * BB * (D / 4) / 256;
 template <int D>
 __global__ void __launch_bounds__(256)
 window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+  wait_for_previous();
   const int cut = p.cut.cut_tiles(p.tiles_k), kv = blockIdx.x / cut, tile = p.cut.cut_tile(blockIdx.x - kv * cut);
   const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
   const int n = QueryRun::of(p.w, k0, k1).tiles<BB>() * p.group, parts = max(1, ceil_div(n, p.cut.chunk(tile)));
@@ -657,12 +661,11 @@ cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   p.ctas_k = (unsigned)p.cut.ctas(p.tiles_k);
   auto *dq = static_cast<__nv_bfloat16*>(a.dq), *dk = static_cast<__nv_bfloat16*>(a.dk),
        *dv = static_cast<__nv_bfloat16*>(a.dv);
-  window_bwd_kernel<D><<<p.ctas_k + (unsigned)(p.heads * p.tiles_q), kThreads, smem, s>>>(mq, mk, mv, mo, p, dq, dk, dv,
-                                                                                        a.err);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (const int cut = p.cut.cut_tiles(p.tiles_k))
-    window_join_kernel<D><<<dim3(a.B * a.Hk * cut, kJoinCtas<D>), 256, 0, s>>>(p, dk, dv);
-  return cudaGetLastError();
+  e = launch_next(window_bwd_kernel<D>, p.ctas_k + (unsigned)(p.heads * p.tiles_q), kThreads, smem, s, mq, mk, mv, mo, p,
+                  dq, dk, dv, a.err);
+  if (e != cudaSuccess) return e;
+  const int cut = p.cut.cut_tiles(p.tiles_k);
+  return cut ? launch_next(window_join_kernel<D>, dim3(a.B * a.Hk * cut, kJoinCtas<D>), 256, 0, s, p, dk, dv) : e;
 }
 
 }  // namespace

@@ -146,6 +146,7 @@ __device__ __forceinline__ void join(float* part, float* pm, float* pl, int rows
 template <typename T, int D>
 __global__ void __launch_bounds__(D)
 decode_join_kernel(const DecodeAttn a) {
+  wait_for_previous();
   const size_t rows = (size_t)a.B * a.H * a.Nq, row = blockIdx.x;
   const float2* ml = reinterpret_cast<const float2*>(a.ws + a.groups * rows * D);
   float m = -INFINITY;
@@ -209,6 +210,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * kWarpsMma, 1)
 window_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const DecodeAttn a) {
+  let_next_start();
   using R = Ring<D>;
   constexpr int ROWS = 16, K = R::kKeys, KT = K / 8, kWarps = kWarpsMma, ST = R::kStages;
   constexpr int KS = D / 32;      // 16-byte reads of a key row per lane
@@ -415,6 +417,7 @@ window_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_c
 template <int D>
 __global__ void __launch_bounds__(32 * kWarpsF32, 2)
 window_decode_f32_kernel(const DecodeAttn a) {
+  let_next_start();
   constexpr int kWarps = kWarpsF32, kThreads = 32 * kWarps;
   constexpr int ROWS = 256 / D, K = 8, X = D / 16;  // as many rows as registers hold
   __shared__ __align__(16) float part[kWarps * ROWS * D];
@@ -558,8 +561,7 @@ cudaError_t launch_d(const DecodeAttn& a, const DecodePlan& plan, cudaStream_t s
     e = launch(window_decode_f32_kernel<D>, a, plan, 32 * kWarpsF32, 0, s, a);
   }
   if (e != cudaSuccess || plan.groups == 1) return e;
-  decode_join_kernel<T, D><<<(unsigned)(a.B * a.H * a.Nq), D, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_next(decode_join_kernel<T, D>, (unsigned)(a.B * a.H * a.Nq), D, 0, s, a);
 }
 
 }  // namespace

@@ -352,6 +352,8 @@ __device__ __forceinline__ void dkdv_tile(const BwdSimt& a, unsigned i) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 window_bwd_simt_kernel(const BwdSimt a) {
+  let_next_start();
+  wait_for_previous();
   if (blockIdx.x < a.ctas_k)
     dkdv_tile<D>(a, blockIdx.x);
   else
@@ -384,6 +386,7 @@ __device__ __forceinline__ void join(const BwdSimt& a, const float* __restrict__
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 window_join_simt_kernel(const BwdSimt a, long long rows_k, long long rows_q, float* dk, float* dv, float* dq) {
+  wait_for_previous();
   constexpr int V = D / 4;
   long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i < rows_k * V) return join<D, true>(a, a.dk, rows_k, i, dk);
@@ -429,14 +432,11 @@ cudaError_t bwd_d(const WindowAttn& a, cudaStream_t s) {
   p.dv = cut_k ? p.dk + p.cut.chunks_k * rk * D : dv;
   p.ctas_k = (unsigned)(p.heads_k * ceil_div(a.w.Nk, T)) * p.cut.chunks_k;
   const unsigned ctas_q = (unsigned)(p.heads_q * ceil_div(a.w.Nq, T)) * p.cut.chunks_q;
-  window_bwd_simt_kernel<D><<<p.ctas_k + ctas_q, kThreads, smem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (cut_q || cut_k) {
-    const long long rows = (cut_k ? 2 * rk : 0) + (cut_q ? rq : 0);
-    window_join_simt_kernel<D><<<(unsigned)((rows * (D / 4) + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-        p, cut_k ? rk : 0, cut_q ? rq : 0, dk, dv, dq);
-  }
-  return cudaGetLastError();
+  e = launch_next(window_bwd_simt_kernel<D>, p.ctas_k + ctas_q, kThreads, smem, s, p);
+  if (e != cudaSuccess || (!cut_q && !cut_k)) return e;
+  const long long rows = (cut_k ? 2 * rk : 0) + (cut_q ? rq : 0);
+  return launch_next(window_join_simt_kernel<D>, (unsigned)((rows * (D / 4) + kThreads - 1) / kThreads), kThreads, 0, s,
+                     p, cut_k ? rk : 0, cut_q ? rq : 0, dk, dv, dq);
 }
 
 }  // namespace
