@@ -37,10 +37,11 @@
 //
 // Measured, 17,776 tokens, 8 heads, D = 64, every token in sight of 5,400 others
 // and a prefix of 226, each kind alone: dq 430 us (511 with one buffer of S), dkdv
-// 470 (617); exp2 keeps its unit and the MMAs the tensor cores (N = 64 costs them
-// as much as N = 128) half of the time each, and the two do not overlap in full.
-// A delay of half the warps by a third of a pass, so that one half computes while
-// the other reads, costs 5 %.  48 heads: 4.9 ms in all (575 TFLOP/s).
+// 470 (617).  A pair of dq takes 1,990 cycles: exp2 1,024 on its unit, the MMAs 1,024
+// (4 products), and the pass some 640 beside exp2 for waiting, reading tensor
+// memory and handing over, which its two warps per scheduler, in phase, do not
+// cover.  A delay of half the warps by a third of a pass, so that one half computes
+// while the other reads, costs 5 %.  48 heads: 4.9 ms in all (575 TFLOP/s).
 // 8,192 tokens, 16 query heads on 4, D = 128, causal over 2,048, four sinks: dq
 // 229 us, dkdv 270 (357 with the sinks' tile uncut and last, 376 with dP ahead
 // of the gradients), 0.47 ms in all (640 TFLOP/s); causal without a window
