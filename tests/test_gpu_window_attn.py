@@ -350,3 +350,62 @@ def test_decode_is_the_forward_of_the_last_tokens():
     last = ops.window_attn_decode(q[:, :, -2:].contiguous(), k, v, n, 300, 9)
     ops.device_status()
     assert torch.allclose(last, full[:, :, -2:], rtol=0, atol=2e-5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_backward_chains_on_two_streams_and_in_a_graph(D, dtype):
+    # row terms, gradients in parts and their join: each launch starts while the one before it ends
+    q, k, v, do = make(1, 8, 2, 1100, 1100, D, dtype, seed=D)
+    out, lse = ops.window_attn_fwd(q, k, v, 150, 0, 130)
+
+    def run():
+        return ops.window_attn_bwd(q, k, v, out, do, lse, 150, 0, 130)
+
+    want = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(6):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(run())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[0]):
+        first = run()
+        second = run()
+    for _ in range(3):
+        for t in first + second:
+            t.fill_(float("nan"))
+        g.replay()
+        got.append(run())  # behind the replay, on the current stream
+        torch.cuda.synchronize()
+        got += [[t.clone() for t in first], [t.clone() for t in second]]
+    ops.device_status()
+    assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))
+
+
+def test_decode_chains_on_two_streams_and_in_a_graph():
+    # 40 heads of 20,000 keys: shares in a workspace and their join
+    q = torch.randn(1, 40, 1, 128, device="cuda", dtype=torch.bfloat16)
+    kc, vc = (torch.randn(1, 40, 20000, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    n = torch.tensor([19990], dtype=torch.int32, device="cuda")
+    run = lambda: ops.window_attn_decode(q, kc, vc, n, 18000, 500)  # noqa: E731
+    want = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(run())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[1]):
+        first, second = run(), run()
+    g.replay()
+    torch.cuda.synchronize()
+    ops.device_status()
+    assert all(torch.equal(a, want) for a in got + [first, second])
+    check = ops.window_attn_fwd(q, kc[:, :, :19990].contiguous(), vc[:, :, :19990].contiguous(), 18000, 0, 500)[0]
+    # two computations of one value in bf16: weights and output rounded in each, 2^-8 of a value at most
+    assert float((check.double() - want.double()).norm() / want.double().norm()) <= 2.0 ** -7
