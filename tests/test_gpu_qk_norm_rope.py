@@ -302,3 +302,32 @@ def test_captured_and_other_stream():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_offsets_past_32_bits():
+    # 2^31 elements and more: the last tokens against the same tokens alone, saved codes among them
+    N, H, D, n = 270_000, 64, 128, 1003
+    torch.manual_seed(0)
+    xq, dq = (torch.empty(1, N, H, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    for t in (xq, dq):
+        for i in range(0, N, 30_000):
+            t[0, i:i + 30_000].normal_()
+    dq = dq.view(1, H, N, D)
+    xk, dk = xq[:, :, :1], dq[:, :1]
+    wq, wk = torch.rand(D, device="cuda") + 0.5, torch.rand(D, device="cuda") + 0.5
+    plan = ops.RopePlan((torch.arange(N) % 4096)[:, None], (D // 2,))
+    end = plan.at(plan.pos[0, -n:])
+    tail = [t[:, -n:].contiguous() for t in (xq, xk)] + [t[:, :, -n:].contiguous() for t in (dq, dk)]
+    got = ops.qk_norm_rope(xq, xk, wq, wk, plan, save8=True)
+    want = ops.qk_norm_rope(tail[0], tail[1], wq, wk, end, save8=True)
+    assert torch.equal(got[0][:, :, -n:], want[0]) and torch.equal(got[1][:, :, -n:], want[1])
+    assert torch.equal(got[2].codes[:, -n:], want[2].codes) and torch.equal(got[2].scales[:, -n:], want[2].scales)
+    assert torch.equal(ops.unpack8(got[2])[:, -n:], ops.unpack8(want[2]))
+    assert torch.equal(ops.pack8(xq).codes[:, -n:], want[2].codes)
+    for x8, end8 in (((xq, xk), tail[:2]), (got[2:], want[2:])):
+        d = ops.qk_norm_rope_bwd(dq, dk.contiguous(), *x8, wq, wk, plan)
+        e = ops.qk_norm_rope_bwd(tail[2], tail[3], *end8, wq, wk, end)
+        assert torch.equal(d[0][:, -n:], e[0]) and torch.equal(d[1][:, -n:], e[1])
+    ops.device_status()
+    del xq, dq, xk, dk, tail, got, want, x8, end8, d, e, t
+    torch.cuda.empty_cache()

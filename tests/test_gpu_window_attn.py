@@ -409,3 +409,29 @@ def test_decode_chains_on_two_streams_and_in_a_graph():
     check = ops.window_attn_fwd(q, kc[:, :, :19990].contiguous(), vc[:, :, :19990].contiguous(), 18000, 0, 500)[0]
     # two computations of one value in bf16: weights and output rounded in each, 2^-8 of a value at most
     assert float((check.double() - want.double()).norm() / want.double().norm()) <= 2.0 ** -7
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    # 2^31 elements and more in every tensor: the last head against the same head alone
+    H, N, D = 34, 500_000, 128
+    torch.manual_seed(0)
+    q, k, v, do = (torch.empty(1, H, N, D, device="cuda", dtype=dtype) for _ in range(4))
+    for t in (q, k, v, do):
+        for h in range(H):
+            t[0, h].normal_()
+    last = [t[:, -1:].clone() for t in (q, k, v, do)]
+    mask = dict(left=40, right=3, sink=2)
+    out, lse = ops.window_attn_fwd(q, k, v, **mask)
+    one, one_lse = ops.window_attn_fwd(*last[:3], **mask)
+    assert torch.equal(out[:, -1:], one) and torch.equal(lse[:, -1:], one_lse)
+    n = torch.tensor([N - 7], dtype=torch.int32, device="cuda")
+    assert torch.equal(ops.window_attn_decode(q[:, :, -1:].contiguous(), k, v, n, 300, 2)[:, -1:],
+                       ops.window_attn_decode(last[0][:, :, -1:].contiguous(), last[1], last[2], n, 300, 2))
+    got = ops.window_attn_bwd(q, k, v, out, do, lse, **mask)
+    want = ops.window_attn_bwd(*last[:3], one, last[3], one_lse, **mask)
+    ops.device_status()
+    for a, b in zip(got, want):  # the sinks' rows are cut differently: the order of their sums is another
+        assert torch.equal(a[:, -1:, 128:], b[:, :, 128:])
+    del q, k, v, do, last, out, lse, got, want, one, a, b, t
+    torch.cuda.empty_cache()
