@@ -31,6 +31,10 @@
 // fp32: dot products on CUDA cores, four lanes per key; each lane group of
 // four keeps the softmax of its own keys.
 //
+// Measured, D = 128, bf16, calls back to back: one stream, 40 heads of 32,400 keys
+// 116 us (5.7 TB/s), 32 streams of 4,100 keys, 32 heads on 8, 89 us (6.0); with L2
+// flushed between calls 130 and 106.
+//
 // Rows of the cache that no query sees may hold anything: a step may bring some
 // in behind the end of a run (bf16), but their scores become -inf and their
 // values 0 before use.

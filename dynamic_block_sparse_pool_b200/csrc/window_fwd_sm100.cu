@@ -9,7 +9,7 @@
 // then l and O are rescaled: P stays below 2^16, where bf16 and fp32 are as
 // precise as below 1, and O and l share the reference, so the result is the
 // softmax all the same.  P is rounded to bf16 for the second product (at most
-// half a step, 2^-9 of each weight; l sums the unrounded values).
+// half a step, 2^-8 of each weight; l sums the unrounded values).
 //
 // An item is two neighbouring tiles of 128 queries of one head (one, where
 // items would not fill the SMs), so a key tile in shared memory serves both
