@@ -19,6 +19,9 @@ from . import ops
 from .ops import Act8
 
 
+_MOST_NEW = 128  # tokens that window_attn_decode takes of each stream
+
+
 class Mask(NamedTuple):
     """Key u is visible at position t iff u <= t + right and (u < sink or
     u >= t - left); a negative bound is no bound."""
@@ -94,8 +97,11 @@ class Stream:
 
     step() takes the newest tokens' qkv [B, n, H + 2 Hk, D] and their
     positions, appends their keys and values and returns their outputs
-    [B, H, n, D].  Every stream grows by the same n per step; `lens` (device)
-    is what the kernel reads."""
+    [B, H, n, D].  n is any number, a whole prompt's too: the cached attention
+    takes 128 new tokens a call, so more are attended to in pieces.  A step
+    that is refused leaves the stream as it was.  Every stream grows by the
+    same n per step; `lens` (device) is what the kernel reads, `length` the
+    same number on the host, so a step cannot be captured and replayed."""
 
     def __init__(self, B: int, heads: int, key_heads: int, capacity: int, head_dim: int,
                  plan: ops.RopePlan, mask: Mask, wq: Optional[torch.Tensor] = None,
@@ -112,13 +118,32 @@ class Stream:
         self.length = 0
 
     def step(self, qkv: torch.Tensor, pos: torch.Tensor) -> torch.Tensor:
-        xq, xk, xv = _split(qkv, self.heads)
+        B, Hk, capacity, D = self.k.shape
+        want = (B, self.heads + 2 * Hk, D)
+        if qkv.dim() != 4 or (qkv.shape[0], *qkv.shape[2:]) != want or qkv.dtype != self.k.dtype \
+                or qkv.device != self.k.device:
+            raise ValueError(f"a step of this stream takes {want[0]} x n x {want[1]} x {D} values of {self.k.dtype} "
+                             f"on {self.k.device}")
         n = qkv.shape[1]
-        if self.length + n > self.k.shape[2]:
-            raise ValueError(f"{self.length} + {n} tokens exceed the capacity of {self.k.shape[2]}")
+        if self.length + n > capacity:
+            raise ValueError(f"{self.length} + {n} tokens exceed the capacity of {capacity}")
+        xq, xk, xv = _split(qkv, self.heads)
         q, k = ops.qk_norm_rope(xq, xk, self.wq, self.wk, self.plan.at(pos), self.eps)
+        if n == 0:
+            return q
+        # rows past `lens` are not read: they count once every piece is on its way
         self.k[:, :, self.length:self.length + n] = k
         self.v[:, :, self.length:self.length + n] = xv.transpose(1, 2)
+        outs, at = [], 0
+        try:
+            for piece in q.split(_MOST_NEW, 2):
+                self.lens += piece.shape[2]
+                at += piece.shape[2]
+                outs.append(ops.window_attn_decode(piece.contiguous(), self.k, self.v, self.lens, self.mask.left,
+                                                   self.mask.sink, self.scale))
+            out = outs[0] if len(outs) == 1 else torch.cat(outs, 2)
+        except BaseException:
+            self.lens -= at
+            raise
         self.length += n
-        self.lens += n
-        return ops.window_attn_decode(q, self.k, self.v, self.lens, self.mask.left, self.mask.sink, self.scale)
+        return out
