@@ -371,9 +371,10 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tmQ, const CUtensorMa
     const bool valid = q0 + row < q1;
     const size_t tok = (size_t)bh * p.w.Nq + q0 + row;
     // -lse (base 2) and -delta of the row; rows past the last query, and rows
-    // that see no key, get -inf, so their P is 0
+    // that see no key, get -inf, so their P is 0 (lse = NaN, from a NaN that the
+    // row met, stays: its P is NaN)
     const float ls = valid ? p.lse[tok] : -INFINITY;
-    const float nl = ls > -INFINITY ? -ls * kLog2e : -INFINITY, nd = valid ? -p.delta[tok] : 0.f;
+    const float nl = ls != -INFINITY ? -ls * kLog2e : -INFINITY, nd = valid ? -p.delta[tok] : 0.f;
     const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), nl2 = pack_f32x2(nl, nl), nd2 = pack_f32x2(nd, nd);
     const int t = p.w.off + q0 + row, hi = p.w.hi(t), lo = p.w.lo(t);
     bool ok = true;
@@ -508,7 +509,7 @@ __device__ __forceinline__ void dkdv_tile(const CUtensorMap& tmQ, const CUtensor
       const bool whole = all_visible(p.w, q0, min(q0 + BB, p.w.Nq), k0, k1);
       float* nl = vec + (it & 1) * 2 * BB;
       float* nd = nl + BB;
-      (wt < 64 ? nl : nd)[64 * h + (wt & 63)] = wt >= 64 ? -next : next > -INFINITY ? -next * kLog2e : -INFINITY;
+      (wt < 64 ? nl : nd)[64 * h + (wt & 63)] = wt >= 64 ? -next : next != -INFINITY ? -next * kLog2e : -INFINITY;
       if (++qi == per) {
         qi = 0;
         ++g;

@@ -203,7 +203,8 @@ window_fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k,
 }
 
 // P and dS of a 64 x 64 tile; hidden pairs, and rows without keys (lse =
-// -inf), have both 0.
+// -inf), have both 0.  (A row that met a NaN has lse = NaN, which is not
+// without keys: its P and dS are NaN.)
 __device__ __forceinline__ void weights(const float (&s)[4][4], const float (&dp)[4][4], float (&p)[4][4],
                                         float (&ds)[4][4], const Window& w, int q0, int k0, bool whole, float scale,
                                         const float* lse, const float* delta, int ty, int tx) {
@@ -214,8 +215,8 @@ __device__ __forceinline__ void weights(const float (&s)[4][4], const float (&dp
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const bool in = whole || sees(w, w.off + q0 + r, k0 + tx + 16 * b);
-      p[a][b] = in && ls > -INFINITY ? expf(fmaf(scale, s[a][b], -ls)) : 0.f;
-      ds[a][b] = in && ls > -INFINITY ? p[a][b] * (dp[a][b] - de) : 0.f;
+      p[a][b] = in && ls != -INFINITY ? expf(fmaf(scale, s[a][b], -ls)) : 0.f;
+      ds[a][b] = in && ls != -INFINITY ? p[a][b] * (dp[a][b] - de) : 0.f;
     }
   }
 }
