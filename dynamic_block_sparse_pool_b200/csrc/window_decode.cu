@@ -77,8 +77,13 @@ __device__ __forceinline__ bool sees(int t, int u, int left, int sink) {
   return u <= t && (u < sink || u >= t - left);
 }
 
+// A share's maximum as it is handed on: one whose every score was NaN has none,
+// but its sum shows that it is not a share without keys (a maximum ignores NaN).
+__device__ __forceinline__ float share_max(float m, float l) { return l == l ? m : l; }
+
 // The warps' rows, their maxima and sums in shared memory -> the outputs.
-// part: [kWarps][ROWS][D] outputs relative to m, m and l: [kWarps][ROWS].
+// part: [kWarps][ROWS][D] outputs relative to m, m and l: [kWarps][ROWS]; m is
+// -inf where there were no keys and NaN where l is (share_max).
 // Warp 0's place then holds the CTA's, and each CTA of the cluster finishes
 // its share of the rows from all of them.
 template <typename T, int D, int ROWS, int kWarps>
@@ -111,7 +116,7 @@ __device__ __forceinline__ void join(float* part, float* pm, float* pl, int rows
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       l += pm[w * ROWS + r] == -INFINITY ? 0.f : pl[w * ROWS + r] * exp2f(pm[w * ROWS + r] - m);
-    pm[r] = m;
+    pm[r] = share_max(m, l);
     pl[r] = l;
   }
   cluster.sync();
@@ -132,7 +137,8 @@ __device__ __forceinline__ void join(float* part, float* pm, float* pl, int rows
     if (a.groups > 1) {  // this CTA's share, for decode_join_kernel
       const size_t at = (size_t)blockIdx.z * a.B * a.H * a.Nq + row;
       *reinterpret_cast<float4*>(a.ws + at * D + d) = acc;
-      if (d == 0) reinterpret_cast<float2*>(a.ws + (size_t)a.groups * a.B * a.H * a.Nq * D)[at] = make_float2(m, l);
+      if (d == 0)
+        reinterpret_cast<float2*>(a.ws + (size_t)a.groups * a.B * a.H * a.Nq * D)[at] = make_float2(share_max(m, l), l);
       continue;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -408,8 +414,8 @@ window_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_c
     }
   }
   if (c == 0) {
-    pm[warp * ROWS + g] = ma;
-    pm[warp * ROWS + g + 8] = mb;
+    pm[warp * ROWS + g] = share_max(ma, la);
+    pm[warp * ROWS + g + 8] = share_max(mb, lb);
     pl[warp * ROWS + g] = la;
     pl[warp * ROWS + g + 8] = lb;
   }
@@ -510,7 +516,7 @@ window_decode_f32_kernel(const DecodeAttn a) {
       if (g == 0) part[(warp * ROWS + r) * D + 16 * (i >> 2) + 4 * c + (i & 3)] = v;
     }
     if (lane == 0) {
-      pm[warp * ROWS + r] = top;
+      pm[warp * ROWS + r] = share_max(top, sum);
       pl[warp * ROWS + r] = sum;
     }
   }
