@@ -688,11 +688,13 @@ BwdChunks bwd_chunks(int B, int H, int Hk, const Window& w) {
     int& l = longest[t >= c.sink_tiles];
     l = std::max(l, n);
   }
-  const int share = (int)std::max<long long>(8, (all * B * Hk + 147) / 148);
+  // (beyond 32 bits for tens of millions of tokens in sight of one another; a tile
+  // that is cut has more pairs than that, so a part always fits)
+  const long long share = std::max<long long>(8, (all * B * Hk + 147) / 148);
   for (int i = 0; i < 2; ++i) {
-    const bool cut = 2ll * longest[i] > 3ll * share;
-    c.chunks[i] = cut ? share : std::max(1, longest[i]);
-    c.counts[i] = cut ? ceil_div(longest[i], share) : 1;
+    const bool cut = 2ll * longest[i] > 3 * share;
+    c.chunks[i] = cut ? (int)share : std::max(1, longest[i]);
+    c.counts[i] = cut ? ceil_div(longest[i], c.chunks[i]) : 1;
   }
   c.heads = B * Hk;
   return c;
