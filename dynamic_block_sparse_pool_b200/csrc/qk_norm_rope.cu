@@ -355,6 +355,9 @@ qk_norm_rope_bwd_kernel(const BwdArgs<TX, TG> a) {
     turn.load(a.rope, b, n, sub, a.err);
     turn.reverse();
     for (int h = ha + slot; h - slot < hz; h += RPW) {
+      // (codes: the copy that starts now goes into the slot whose scale the row's
+      // other threads read a step ago; shuffles do not order those reads before it)
+      if constexpr (sizeof(TX) == 1) __syncwarp();
       fetch_step();
       copy_wait<kDepth - 1>();
       const uint4* from = ring + (rs % kDepth) * (SLOTS * kThreads) + threadIdx.x;
