@@ -31,7 +31,9 @@ dsa_status fail(dsa_status st, const char* fmt, ...) {
 }
 
 dsa_status launched(cudaError_t e, const char* where) {
-  return e == cudaSuccess ? DSA_OK : fail(DSA_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+  if (e == cudaSuccess) return DSA_OK;
+  cudaGetLastError();  // reported here: the next call's launch shall not find it
+  return fail(DSA_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
 dsa_status sm_count(int* n) {

@@ -214,8 +214,9 @@ struct Ring {
   static constexpr int kBytes = kWarpsMma * kStages * kStep;
 };
 
-// Grid: x = cluster size * key heads of all streams, y = tiles of 16 rows, z =
-// groups.
+// Grid: x = cluster size * tiles of 16 rows (up to 2^16 heads of 128 tokens share a
+// key head, more tiles than the other dimensions have places), y = key heads of
+// all streams, z = groups.
 template <int D>
 __global__ void __launch_bounds__(32 * kWarpsMma, 1)
 window_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -233,8 +234,8 @@ window_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_c
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = cluster.num_blocks(), rank = cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int kvh = blockIdx.x / cs, b = kvh / a.Hk, kh = kvh - b * a.Hk;
-  const int all = a.group * a.Nq, row0 = blockIdx.y * ROWS, rows = min(ROWS, all - row0);
+  const int kvh = blockIdx.y, b = kvh / a.Hk, kh = kvh - b * a.Hk;
+  const int all = a.group * a.Nq, row0 = (blockIdx.x / cs) * ROWS, rows = min(ROWS, all - row0);
   const int len = stream_len(a, b);
   const Steps<K> st(len, a.Nq, a.left, a.sink);
   // rows of the group are contiguous in q: (head, token)
@@ -436,8 +437,8 @@ window_decode_f32_kernel(const DecodeAttn a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = cluster.num_blocks(), rank = cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int kvh = blockIdx.x / cs, b = kvh / a.Hk, kh = kvh - b * a.Hk;
-  const int all = a.group * a.Nq, row0 = blockIdx.y * ROWS, rows = min(ROWS, all - row0);
+  const int kvh = blockIdx.y, b = kvh / a.Hk, kh = kvh - b * a.Hk;
+  const int all = a.group * a.Nq, row0 = (blockIdx.x / cs) * ROWS, rows = min(ROWS, all - row0);
   const int len = stream_len(a, b);
   const Steps<K> st(len, a.Nq, a.left, a.sink);
   const size_t q_rows = ((size_t)b * a.H + (size_t)kh * a.group) * a.Nq;
@@ -543,7 +544,7 @@ cudaError_t launch(void (*kernel)(Args...), const DecodeAttn& a, const DecodePla
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.Hk * plan.cluster), (unsigned)plan.tiles, (unsigned)plan.groups);
+  cfg.gridDim = dim3((unsigned)(plan.cluster * plan.tiles), (unsigned)(a.B * a.Hk), (unsigned)plan.groups);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
