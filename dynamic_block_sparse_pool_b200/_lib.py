@@ -40,6 +40,7 @@ SIGNATURES = {
     "dsa_gilbert_order": (_i, [_i, _i, _i, _i, _vp]),
     "dsa_permute_tokens": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
     "dsa_rope_table": (_i, [_i, _i, _f, _vp, _vp]),
+    "dsa_rope_table_f64": (_i, [_i, _i, _vp, _vp, _vp]),
     "dsa_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _f, _vp, _vp,
                               _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "dsa_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp,

@@ -282,17 +282,22 @@ dsa_status dsa_window_attn_decode(const void* q, const void* k, const void* v,
 }
 
 dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table, void* stream) {
+  const double base = theta;
+  return dsa_rope_table_f64(positions, pairs, &base, table, stream);
+}
+
+dsa_status dsa_rope_table_f64(int positions, int pairs, const double* theta, float* table, void* stream) {
   dsa::api_set_last_error("");
-  if (!table) return fail(DSA_ERR_INVALID_ARG, "null table");
+  if (!table || !theta) return fail(DSA_ERR_INVALID_ARG, "null table or theta");
   if (positions < 1 || pairs < 1 || pairs > 64)
     return fail(DSA_ERR_INVALID_ARG, "need positions >= 1 and pairs in 1..64 (got %d, %d)", positions, pairs);
   if ((long long)positions * pairs > (1 << 30)) return fail(DSA_ERR_INVALID_ARG, "the table exceeds 2^30 entries");
-  if (!(theta > 0.f) || !std::isfinite(theta)) return fail(DSA_ERR_INVALID_ARG, "theta must be finite and > 0");
+  if (!(*theta > 0.0) || !std::isfinite(*theta)) return fail(DSA_ERR_INVALID_ARG, "theta must be finite and > 0");
   if (!aligned(table, 8)) return fail(DSA_ERR_INVALID_ARG, "table must be 8-byte aligned");
   unsigned* err = nullptr;
   const dsa_status st = dsa::api_checked_device(&err);
   if (st != DSA_OK) return st;
-  return launched(dsa::launch_rope_table(positions, pairs, theta, reinterpret_cast<float2*>(table),
+  return launched(dsa::launch_rope_table(positions, pairs, *theta, reinterpret_cast<float2*>(table),
                                          static_cast<cudaStream_t>(stream)), "rope_table launch");
 }
 

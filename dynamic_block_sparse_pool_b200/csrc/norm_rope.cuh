@@ -51,7 +51,7 @@ struct NormRopeBwd {
   unsigned* err;
 };
 
-cudaError_t launch_rope_table(int positions, int pairs, float theta, float2* table, cudaStream_t s);
+cudaError_t launch_rope_table(int positions, int pairs, double theta, float2* table, cudaStream_t s);
 cudaError_t launch_qk_norm_rope(const NormRopeFwd& f, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_bwd(const NormRopeBwd& f, cudaStream_t s);
 

@@ -548,7 +548,7 @@ cudaError_t bwd_dispatch(const NormRopeBwd& f, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_rope_table(int positions, int pairs, float theta, float2* table, cudaStream_t s) {
+cudaError_t launch_rope_table(int positions, int pairs, double theta, float2* table, cudaStream_t s) {
   const dim3 block((unsigned)pairs, (unsigned)std::max(1, 128 / pairs));
   rope_table_kernel<<<(unsigned)std::min(ceil_div(positions, (int)block.y), 2048), block, 0, s>>>(positions, pairs, theta,
                                                                                               table);

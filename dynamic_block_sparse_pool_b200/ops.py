@@ -380,8 +380,8 @@ def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None) 
         raise ValueError(f"the rotation tables live on a CUDA device, not on {dev}")
     t = torch.empty(positions, pairs, 2, dtype=torch.float32, device=dev)
     with _on(t):
-        st = lib().dsa_rope_table(positions, pairs, float(theta), t.data_ptr(), _stream(t))
-    check(st, "dsa_rope_table")
+        st = lib().dsa_rope_table_f64(positions, pairs, ctypes.byref(ctypes.c_double(theta)), t.data_ptr(), _stream(t))
+    check(st, "dsa_rope_table_f64")
     return t
 
 

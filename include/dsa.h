@@ -452,6 +452,14 @@ dsa_status dsa_permute_tokens(const void* src, void* dst, dsa_dtype dt, int B, i
 dsa_status dsa_rope_table(int positions, int pairs, float theta, float* table, void* stream);
 
 /*
+ * The same with a base in 64 bits (host, one value): context-scaled bases such
+ * as 10000 * 8^(128/126) are not fp32 numbers, and rounding one moves the angles
+ * of position 100,000 by up to 1e-4.
+ */
+dsa_status dsa_rope_table_f64(int positions, int pairs, const double* theta, float* table,
+                              void* stream);
+
+/*
  * Per-head norms of queries and keys with the position rotation, one pass
  * from the projection's layout to the attention's.  (No counterpart in the
  * papers: the video DiTs they measure normalise and rotate q and k right
