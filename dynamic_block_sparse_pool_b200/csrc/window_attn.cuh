@@ -100,9 +100,22 @@ cudaError_t launch_window_decode(const DecodeAttn& a, const DecodePlan& plan, bo
 cudaError_t launch_window_fwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why);
 cudaError_t launch_window_bwd_sm100(const WindowAttn& a, cudaStream_t s, const char** why);
 // fp32 on CUDA cores
-// Chunks of a gradient tile's pairs, and the floats their shares take.
+// How the pairs of a gradient's tiles are cut into chunks, one CTA each: tiles
+// [from, to) have more than `chunk` of them and leave up to `parts` partial sums
+// (shares) in the workspace; the others are one chunk and need no share.
+struct SimtCut {
+  int chunk, parts, from, to;
+  __host__ __device__ int tiles() const { return to - from; }
+  __host__ __device__ bool shared(int tile) const { return tile >= from && tile < to; }
+  __host__ __device__ size_t slot(int head, int tile, int part) const {
+    return ((size_t)head * tiles() + tile - from) * parts + part;
+  }
+  __host__ __device__ size_t slots(int heads) const { return (size_t)heads * tiles() * parts; }
+};
+// dQ's tiles; those of dK and dV with sinks (0) and without (1).
 struct SimtChunks {
-  int chunk_q, chunks_q, chunk_k, chunks_k;
+  SimtCut q, k[2];
+  int sink_tiles;
 };
 SimtChunks simt_chunks(int B, int H, int Hk, const Window& w);
 size_t simt_share_floats(int B, int H, int Hk, const Window& w, int D);

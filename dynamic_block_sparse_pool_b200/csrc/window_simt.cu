@@ -231,19 +231,41 @@ struct BwdSimt {
   int heads_q, heads_k, group;  // B H, B Hk, H / Hk
   float scale;
   SimtChunks cut;
-  float *dq, *dk, *dv;          // gradients, or the chunks' shares of them
+  float *dq, *dk, *dv;
+  // shares [slot][T][D]: dQ's, and dK's and dV's of the tiles with sinks and of the others
+  float *share_q, *share_k[2], *share_v[2];
   unsigned ctas_k;              // CTAs of dK and dV; the others are dQ's
 };
 
-// Chunk y of the pairs of tile x of all tiles of a gradient: the first chunks of
-// all tiles come first.
+// A chunk of a tile of a gradient: the first chunks of all tiles come first, then
+// layer by layer the further ones of the tiles that have them.
 struct Place {
   int head, tile, y;
-  __device__ __forceinline__ Place(unsigned i, int heads, int tiles) {
-    const unsigned all = (unsigned)heads * tiles, x = i % all;
-    y = (int)(i / all);
-    head = (int)(x / tiles);
-    tile = (int)(x - head * tiles);
+  template <int N>
+  __device__ __forceinline__ Place(unsigned i, int heads, int tiles, const SimtCut (&cut)[N]) : y(0) {
+    unsigned per = (unsigned)heads * tiles, run = tiles;
+    int first = 0;
+    if (i >= per) {
+      i -= per;
+      for (int c = 0; c < N; ++c) {
+        run = cut[c].tiles();
+        per = (unsigned)heads * run;
+        first = cut[c].from;
+        const unsigned n = per * (cut[c].parts - 1);
+        if (i < n) break;
+        i -= n;
+      }
+      y = 1 + (int)(i / per);
+      i %= per;
+    }
+    head = (int)(i / run);
+    tile = first + (int)(i - head * run);
+  }
+  template <int N>
+  static unsigned count(int heads, int tiles, const SimtCut (&cut)[N]) {
+    unsigned n = (unsigned)heads * tiles;
+    for (int c = 0; c < N; ++c) n += (unsigned)heads * cut[c].tiles() * (cut[c].parts - 1);
+    return n;
   }
 };
 
@@ -260,13 +282,13 @@ __device__ __forceinline__ void dq_tile(const BwdSimt& a, unsigned i) {
   extern __shared__ __align__(16) float sm[];
   float *Q = sm, *O = Q + T * P, *K = O + T * P, *V = K + T * P, *W = V + T * P, *ls = W + T * SP, *de = ls + T;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const Place at(i, a.heads_q, ceil_div(w.Nq, T));
+  const SimtCut cuts[1] = {a.cut.q};
+  const Place at(i, a.heads_q, ceil_div(w.Nq, T), cuts);
   const int bh = at.head, q0 = at.tile * T, q1 = min(q0 + T, w.Nq);
   const size_t qh = (size_t)bh * w.Nq * D, kh = (size_t)(bh / a.group) * w.Nk * D;
   const KeyTiles<T> kt = KeyTiles<T>::of(w, q0, q1);
-  const int e0 = at.y * a.cut.chunk_q, e1 = min(kt.count(), e0 + a.cut.chunk_q);
+  const int e0 = at.y * cuts[0].chunk, e1 = min(kt.count(), e0 + cuts[0].chunk);
   if (at.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
-  float* dq = a.dq + at.y * ((size_t)a.heads_q * w.Nq * D);
   stage<D>(Q, q + qh, q0, w.Nq);
   stage<D>(O, dout + qh, q0, w.Nq);
   stage_vec(ls, a.lse + (size_t)bh * w.Nq, q0, w.Nq, -INFINITY);
@@ -290,7 +312,10 @@ __device__ __forceinline__ void dq_tile(const BwdSimt& a, unsigned i) {
     product_nn<D>(acc, W, K, ty, tx);
   }
   float mul[4] = {scale, scale, scale, scale};
-  store_rows<D>(dq + qh, acc, q0, q1, mul, ty, tx);
+  if (cuts[0].shared(at.tile))
+    store_rows<D>(a.share_q + cuts[0].slot(bh, at.tile, at.y) * (T * D), acc, 0, q1 - q0, mul, ty, tx);
+  else
+    store_rows<D>(a.dq + qh, acc, q0, q1, mul, ty, tx);
 }
 
 // dK and dV of a key tile, over the query heads of its key head
@@ -305,14 +330,15 @@ __device__ __forceinline__ void dkdv_tile(const BwdSimt& a, unsigned i) {
   extern __shared__ __align__(16) float sm[];
   float *K = sm, *V = K + T * P, *Q = V + T * P, *O = Q + T * P, *W = O + T * P, *ls = W + T * SP, *de = ls + T;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const Place at(i, a.heads_k, ceil_div(w.Nk, T));
+  const Place at(i, a.heads_k, ceil_div(w.Nk, T), a.cut.k);
+  const int kind = at.tile >= a.cut.sink_tiles;
+  const SimtCut cut = a.cut.k[kind];
   const int kv = at.head, k0 = at.tile * T, k1 = min(k0 + T, w.Nk);
   const size_t kh = (size_t)kv * w.Nk * D;
   const QueryRun run = QueryRun::of(w, k0, k1);
   const int i0 = run.q0 / T, per = run.tiles<T>(), n = per * group;  // query tiles per head, head after head
-  const int e0 = at.y * a.cut.chunk_k, e1 = min(n, e0 + a.cut.chunk_k);
+  const int e0 = at.y * cut.chunk, e1 = min(n, e0 + cut.chunk);
   if (at.y > 0 && e0 >= e1) return;  // (chunk 0 writes its zeros)
-  const size_t share = at.y * ((size_t)a.heads_k * w.Nk * D);
   stage<D>(K, a.k + kh, k0, w.Nk);
   stage<D>(V, a.v + kh, k0, w.Nk);
   float ak[4][D / 16] = {}, av[4][D / 16] = {};
@@ -345,8 +371,14 @@ __device__ __forceinline__ void dkdv_tile(const BwdSimt& a, unsigned i) {
     product_nn<D>(ak, W, Q, ty, tx);
   }
   float one[4] = {1.f, 1.f, 1.f, 1.f}, mul[4] = {scale, scale, scale, scale};
-  store_rows<D>(a.dv + share + kh, av, k0, k1, one, ty, tx);
-  store_rows<D>(a.dk + share + kh, ak, k0, k1, mul, ty, tx);
+  if (cut.shared(at.tile)) {
+    const size_t share = cut.slot(kv, at.tile, at.y) * (T * D);
+    store_rows<D>(a.share_v[kind] + share, av, 0, k1 - k0, one, ty, tx);
+    store_rows<D>(a.share_k[kind] + share, ak, 0, k1 - k0, mul, ty, tx);
+  } else {
+    store_rows<D>(a.dv + kh, av, k0, k1, one, ty, tx);
+    store_rows<D>(a.dk + kh, ak, k0, k1, mul, ty, tx);
+  }
 }
 
 // All gradients: dK's and dV's CTAs, then dQ's, which fill in behind them.
@@ -361,38 +393,46 @@ window_bwd_simt_kernel(const BwdSimt a) {
     dq_tile<D>(a, blockIdx.x - a.ctas_k);
 }
 
-// Sums the chunks' shares of one gradient, [chunks][heads][N][D] -> [heads][N][D];
-// a row of a tile has as many shares as the tile has chunks (at least one).
-// Thread i: four columns of a row.
+// Sums the shares of four columns of a row, i-th of all rows of a gradient's tiles
+// that have shares (a tile as many as it has chunks, at least one).
 template <int D, bool KEYS>
-__device__ __forceinline__ void join(const BwdSimt& a, const float* __restrict__ part, long long rows, long long i,
-                                     float* __restrict__ out) {
-  const long long row = i / (D / 4);
+__device__ __forceinline__ void join(const BwdSimt& a, const SimtCut& cut, const float* __restrict__ shares,
+                                     long long i, float* __restrict__ out) {
+  constexpr int V = D / 4;
   const Window w = a.w;
-  const int N = KEYS ? w.Nk : w.Nq, x0 = (int)(row % N) / T * T, x1 = min(x0 + T, N);
+  const long long row = i / V, t = row / T;
+  const int head = (int)(t / cut.tiles()), tile = cut.from + (int)(t - (long long)head * cut.tiles());
+  const int r = (int)(row - t * T), N = KEYS ? w.Nk : w.Nq, x0 = tile * T, x1 = min(x0 + T, N);
+  if (x0 + r >= x1) return;
   const int n = KEYS ? QueryRun::of(w, x0, x1).tiles<T>() * a.group : KeyTiles<T>::of(w, x0, x1).count();
-  const int chunks = max(1, ceil_div(n, KEYS ? a.cut.chunk_k : a.cut.chunk_q));
-  const float4* p = reinterpret_cast<const float4*>(part) + i;
+  const int chunks = max(1, ceil_div(n, cut.chunk));
+  const float4* p = reinterpret_cast<const float4*>(shares + (cut.slot(head, tile, 0) * T + r) * D) + i % V;
   float4 s = *p;
 #pragma unroll 4
   for (int c = 1; c < chunks; ++c) {
-    p += rows * (D / 4);
+    p += T * V;
     const float4 x = *p;
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
-  reinterpret_cast<float4*>(out)[i] = s;
+  reinterpret_cast<float4*>(out + ((size_t)head * N + x0 + r) * D)[i % V] = s;
 }
 
-// The gradients that have shares: rows_k of dK and of dV, rows_q of dQ (0: none).
+// All gradients that have shares, one after another.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-window_join_simt_kernel(const BwdSimt a, long long rows_k, long long rows_q, float* dk, float* dv, float* dq) {
+window_join_simt_kernel(const BwdSimt a) {
   wait_for_previous();
   constexpr int V = D / 4;
   long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i < rows_k * V) return join<D, true>(a, a.dk, rows_k, i, dk);
-  if ((i -= rows_k * V) < rows_k * V) return join<D, true>(a, a.dv, rows_k, i, dv);
-  if ((i -= rows_k * V) < rows_q * V) join<D, false>(a, a.dq, rows_q, i, dq);
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const SimtCut& cut = a.cut.k[kind];
+    const long long n = (long long)a.heads_k * cut.tiles() * (T * V);
+    if (i < n) return join<D, true>(a, cut, a.share_k[kind], i, a.dk);
+    if ((i -= n) < n) return join<D, true>(a, cut, a.share_v[kind], i, a.dv);
+    i -= n;
+  }
+  if (i < (long long)a.heads_q * a.cut.q.tiles() * (T * V)) join<D, false>(a, a.cut.q, a.share_q, i, a.dq);
 }
 
 template <int D>
@@ -411,7 +451,6 @@ cudaError_t bwd_d(const WindowAttn& a, cudaStream_t s) {
   const size_t smem = (4 * T * padded<D>() + T * SP + 2 * T) * sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(window_bwd_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  float *dq = static_cast<float*>(a.dq), *dk = static_cast<float*>(a.dk), *dv = static_cast<float*>(a.dv);
   BwdSimt p;
   p.q = static_cast<const float*>(a.q);
   p.k = static_cast<const float*>(a.k);
@@ -425,57 +464,73 @@ cudaError_t bwd_d(const WindowAttn& a, cudaStream_t s) {
   p.group = a.H / a.Hk;
   p.scale = a.scale;
   p.cut = simt_chunks(a.B, a.H, a.Hk, a.w);
-  const long long rq = (long long)p.heads_q * a.w.Nq, rk = (long long)p.heads_k * a.w.Nk;
-  const bool cut_q = p.cut.chunks_q > 1, cut_k = p.cut.chunks_k > 1;
-  // shares: dQ's, dK's, dV's, each where it has more than one
-  p.dq = cut_q ? a.shares : dq;
-  p.dk = cut_k ? a.shares + (cut_q ? p.cut.chunks_q * rq * D : 0) : dk;
-  p.dv = cut_k ? p.dk + p.cut.chunks_k * rk * D : dv;
-  p.ctas_k = (unsigned)(p.heads_k * ceil_div(a.w.Nk, T)) * p.cut.chunks_k;
-  const unsigned ctas_q = (unsigned)(p.heads_q * ceil_div(a.w.Nq, T)) * p.cut.chunks_q;
+  p.dq = static_cast<float*>(a.dq);
+  p.dk = static_cast<float*>(a.dk);
+  p.dv = static_cast<float*>(a.dv);
+  long long rows = 0;  // to be joined
+  float* at = a.shares;
+  auto room = [&](const SimtCut& c, int heads) {
+    float* here = at;
+    at += c.slots(heads) * (T * D);
+    rows += (long long)heads * c.tiles() * T;
+    return here;
+  };
+  p.share_q = room(p.cut.q, p.heads_q);
+  for (int kind = 0; kind < 2; ++kind) {
+    p.share_k[kind] = room(p.cut.k[kind], p.heads_k);
+    p.share_v[kind] = room(p.cut.k[kind], p.heads_k);
+  }
+  const SimtCut cut_q[1] = {p.cut.q};
+  p.ctas_k = Place::count(p.heads_k, ceil_div(a.w.Nk, T), p.cut.k);
+  const unsigned ctas_q = Place::count(p.heads_q, ceil_div(a.w.Nq, T), cut_q);
   e = launch_next(window_bwd_simt_kernel<D>, p.ctas_k + ctas_q, kThreads, smem, s, p);
-  if (e != cudaSuccess || (!cut_q && !cut_k)) return e;
-  const long long rows = (cut_k ? 2 * rk : 0) + (cut_q ? rq : 0);
+  if (e != cudaSuccess || rows == 0) return e;
   return launch_next(window_join_simt_kernel<D>, (unsigned)((rows * (D / 4) + kThreads - 1) / kThreads), kThreads, 0, s,
-                     p, cut_k ? rk : 0, cut_q ? rq : 0, dk, dv, dq);
+                     p);
 }
 
 }  // namespace
 
 // The chunks of tile pairs: as long as a third of an SM's share of all pairs
 // (half: 3 % slower, a quarter: the same where pairs are many, 6 % slower where they are
-// few); one chunk where the longest tile is at most half as long again.
+// few); one chunk where the longest tile is at most half as long again.  Key tiles
+// with sinks, which far more queries see, are judged apart from the others, and
+// only tiles with more than one chunk have shares: with shares for every tile of a
+// gradient, 100,000 tokens, one head, D = 128, causal over 1,000 with four sinks took
+// 2.56 GB of workspace for 0.10 GB of gradients (now 2 MB).
 SimtChunks simt_chunks(int B, int H, int Hk, const Window& w) {
-  auto cut = [](long long heads, int tiles, auto count, int& chunk, int& chunks) {
-    long long all = 0;
+  auto cut = [](long long share, int t0, int t1, auto count) {
     int longest = 1;
-    for (int t = 0; t < tiles; ++t) {
-      const int n = count(t);
-      all += n;
-      longest = std::max(longest, n);
-    }
-    const long long share = std::max(1ll, (all * heads + 443) / 444);
-    chunk = longest;
-    chunks = 1;
+    for (int t = t0; t < t1; ++t) longest = std::max(longest, count(t));
+    SimtCut c = {longest, 1, t0, t0};
     if (2ll * longest > 3 * share) {
-      chunk = (int)share;
-      chunks = ceil_div(longest, chunk);
+      c.chunk = (int)share;
+      c.parts = ceil_div(longest, c.chunk);
+      while (count(c.from) <= c.chunk) ++c.from;  // (the longest tile stops both)
+      for (c.to = t1; count(c.to - 1) <= c.chunk;) --c.to;
     }
+    return c;
   };
+  auto share = [](long long heads, int tiles, auto count) {
+    long long all = 0;
+    for (int t = 0; t < tiles; ++t) all += count(t);
+    return std::max(1ll, (all * heads + 443) / 444);
+  };
+  const int group = H / Hk, tq = ceil_div(w.Nq, T), tk = ceil_div(w.Nk, T);
+  auto keys = [&](int t) { return KeyTiles<T>::of(w, t * T, std::min((t + 1) * T, w.Nq)).count(); };
+  auto queries = [&](int t) { return QueryRun::of(w, t * T, std::min((t + 1) * T, w.Nk)).tiles<T>() * group; };
   SimtChunks c;
-  const int group = H / Hk;
-  cut((long long)B * H, ceil_div(w.Nq, T),
-      [&](int t) { return KeyTiles<T>::of(w, t * T, std::min((t + 1) * T, w.Nq)).count(); }, c.chunk_q, c.chunks_q);
-  cut((long long)B * Hk, ceil_div(w.Nk, T),
-      [&](int t) { return QueryRun::of(w, t * T, std::min((t + 1) * T, w.Nk)).tiles<T>() * group; }, c.chunk_k,
-      c.chunks_k);
+  c.sink_tiles = ceil_div(w.sink, T);
+  c.q = cut(share((long long)B * H, tq, keys), 0, tq, keys);
+  const long long sk = share((long long)B * Hk, tk, queries);
+  c.k[0] = cut(sk, 0, c.sink_tiles, queries);
+  c.k[1] = cut(sk, c.sink_tiles, tk, queries);
   return c;
 }
 
 size_t simt_share_floats(int B, int H, int Hk, const Window& w, int D) {
   const SimtChunks c = simt_chunks(B, H, Hk, w);
-  return ((c.chunks_q > 1 ? (size_t)c.chunks_q * B * H * w.Nq : 0) +
-          (c.chunks_k > 1 ? (size_t)c.chunks_k * 2 * B * Hk * w.Nk : 0)) * D;
+  return (c.q.slots(B * H) + 2 * (c.k[0].slots(B * Hk) + c.k[1].slots(B * Hk))) * (T * D);
 }
 
 cudaError_t launch_window_fwd_simt(const WindowAttn& a, cudaStream_t s) {
