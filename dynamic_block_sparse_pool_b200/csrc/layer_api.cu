@@ -149,7 +149,7 @@ size_t delta_bytes(const dsa::WindowAttn& a) { return ((size_t)a.B * a.H * a.w.N
 
 size_t window_bwd_bytes(const dsa::WindowAttn& a, dsa_dtype dt) {
   if (dt == DSA_F32) return delta_bytes(a) + dsa::simt_share_floats(a.B, a.H, a.Hk, a.w, a.D) * sizeof(float);
-  const size_t slots = dsa::bwd_chunks(a.B, a.H, a.Hk, a.w).slots((a.w.Nk + 127) / 128);
+  const size_t slots = dsa::bwd_cut(a.B, a.H, a.Hk, a.w).slots();
   return delta_bytes(a) + slots * 2 * 128 * a.D * sizeof(float);
 }
 

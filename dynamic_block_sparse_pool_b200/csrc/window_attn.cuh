@@ -29,23 +29,32 @@ struct BwdChunks {
     head = i / per;
     tile = (k ? sink_tiles : 0) + i - head * per;
   }
-  // tiles of a head that are cut, and the i-th of them
-  __host__ __device__ int cut_tiles(int tiles) const {
-    return (counts[0] > 1 ? sink_tiles : 0) + (counts[1] > 1 ? tiles - sink_tiles : 0);
-  }
-  __host__ __device__ int cut_tile(int i) const { return counts[0] > 1 ? i : sink_tiles + i; }
-  // place of a part's share: the cut kinds one after the other
-  __host__ __device__ size_t slot(int head, int tiles, int tile, int part) const {
-    const size_t first = counts[0] > 1 ? (size_t)heads * sink_tiles * counts[0] : 0;
-    if (tile < sink_tiles) return ((size_t)head * sink_tiles + tile) * counts[0] + part;
-    return first + ((size_t)head * (tiles - sink_tiles) + tile - sink_tiles) * counts[1] + part;
-  }
-  __host__ __device__ size_t slots(int tiles) const {
-    return (size_t)heads * ((counts[0] > 1 ? (size_t)sink_tiles * counts[0] : 0) +
-                            (counts[1] > 1 ? (size_t)(tiles - sink_tiles) * counts[1] : 0));
-  }
 };
 BwdChunks bwd_chunks(int B, int H, int Hk, const Window& w);
+
+// The same with the tiles that have shares (partial sums in the workspace): of
+// each kind those from the first with more than one part to the last, which few
+// queries over a long past make a small run of all tiles.
+struct BwdCut : BwdChunks {
+  int from[2], to[2];
+  __host__ __device__ int run(bool k) const { return k ? to[1] - from[1] : to[0] - from[0]; }
+  __host__ __device__ bool shared(int tile) const {
+    return kind(tile) ? tile >= from[1] && tile < to[1] : tile >= from[0] && tile < to[0];
+  }
+  // tiles of a head that have shares, and the i-th of them
+  __host__ __device__ int cut_tiles() const { return run(0) + run(1); }
+  __host__ __device__ int cut_tile(int i) const { return i < run(0) ? from[0] + i : from[1] + i - run(0); }
+  // place of a part's share: the kinds one after the other
+  __host__ __device__ size_t slot(int head, int tile, int part) const {
+    const bool k = kind(tile);
+    const size_t first = k ? (size_t)heads * run(0) * counts[0] : 0;
+    return first + ((size_t)head * run(k) + tile - (k ? from[1] : from[0])) * parts(tile) + part;
+  }
+  __host__ __device__ size_t slots() const {
+    return (size_t)heads * ((size_t)run(0) * counts[0] + (size_t)run(1) * counts[1]);
+  }
+};
+BwdCut bwd_cut(int B, int H, int Hk, const Window& w);
 
 struct WindowAttn {
   int B, H, Hk, D;

@@ -100,7 +100,7 @@ struct Layout {
 
 struct BwdParams {
   Window w;
-  BwdChunks cut;   // dkdv
+  BwdCut cut;      // dkdv
   float* shares;   // dkdv: [slot][dV, dK][128][D]
   int group;       // query heads per key head
   int tiles_q, tiles_k;  // tiles per head
@@ -579,9 +579,9 @@ __device__ __forceinline__ void dkdv_tile(const CUtensorMap& tmQ, const CUtensor
 #pragma unroll
           for (int e = 0; e < 32; ++e) g[e] = 0u;
         }
-        if (p.cut.parts(tile) > 1) {  // this CTA's share, for window_join_kernel
+        if (p.cut.shared(tile)) {  // this CTA's share, for window_join_kernel
           float4* sh = reinterpret_cast<float4*>(
-              p.shares + ((p.cut.slot(kv, p.tiles_k, tile, part) * 2 + h) * BB + row) * D + 32 * g32);
+              p.shares + ((p.cut.slot(kv, tile, part) * 2 + h) * BB + row) * D + 32 * g32);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             sh[x] = make_float4(__uint_as_float(g[4 * x]), __uint_as_float(g[4 * x + 1]), __uint_as_float(g[4 * x + 2]),
@@ -622,7 +622,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
 window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
   wait_for_previous();
-  const int cut = p.cut.cut_tiles(p.tiles_k), kv = blockIdx.x / cut, tile = p.cut.cut_tile(blockIdx.x - kv * cut);
+  const int cut = p.cut.cut_tiles(), kv = blockIdx.x / cut, tile = p.cut.cut_tile(blockIdx.x - kv * cut);
   const int k0 = tile * BB, k1 = min(k0 + BB, p.w.Nk);
   const int n = QueryRun::of(p.w, k0, k1).tiles<BB>() * p.group, parts = max(1, ceil_div(n, p.cut.chunk(tile)));
   const int i = blockIdx.y * 256 + threadIdx.x, h = i / (BB * (D / 4)), r = i / (D / 4) % BB, d = 4 * (i % (D / 4));
@@ -631,7 +631,7 @@ window_join_kernel(const BwdParams p, __nv_bfloat16* __restrict__ dk, __nv_bfloa
 #pragma unroll 4
   for (int c = 0; c < parts; ++c) {
     const float4 x =
-        *reinterpret_cast<const float4*>(p.shares + ((p.cut.slot(kv, p.tiles_k, tile, c) * 2 + h) * BB + r) * D + d);
+        *reinterpret_cast<const float4*>(p.shares + ((p.cut.slot(kv, tile, c) * 2 + h) * BB + r) * D + d);
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
   const float mul = h ? p.scale : 1.f;
@@ -649,7 +649,7 @@ cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   if (e != cudaSuccess) return e;
   BwdParams p;
   p.w = a.w;
-  p.cut = bwd_chunks(a.B, a.H, a.Hk, a.w);
+  p.cut = bwd_cut(a.B, a.H, a.Hk, a.w);
   p.shares = a.shares;
   p.group = a.H / a.Hk;
   p.tiles_q = ceil_div(a.w.Nq, BB);
@@ -666,11 +666,16 @@ cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   e = launch_next(window_bwd_kernel<D>, p.ctas_k + (unsigned)(p.heads * p.tiles_q), kThreads, smem, s, mq, mk, mv, mo, p,
                   dq, dk, dv, a.err);
   if (e != cudaSuccess) return e;
-  const int cut = p.cut.cut_tiles(p.tiles_k);
+  const int cut = p.cut.cut_tiles();
   return cut ? launch_next(window_join_kernel<D>, dim3(a.B * a.Hk * cut, kJoinCtas<D>), 256, 0, s, p, dk, dv) : e;
 }
 
 }  // namespace
+
+// Pairs of a key tile.
+static int tile_pairs(const Window& w, int t, int group) {
+  return QueryRun::of(w, t * BB, std::min((t + 1) * BB, w.Nk)).tiles<BB>() * group;
+}
 
 // A tile with sinks sees every query, the others a window of them: each kind is
 // cut where its longest tile has more than one and a half times an SM's share of
@@ -683,7 +688,7 @@ BwdChunks bwd_chunks(int B, int H, int Hk, const Window& w) {
   int longest[2] = {0, 0};
   long long all = 0;
   for (int t = 0; t < tiles; ++t) {
-    const int n = QueryRun::of(w, t * BB, std::min((t + 1) * BB, w.Nk)).tiles<BB>() * group;
+    const int n = tile_pairs(w, t, group);
     all += n;
     int& l = longest[t >= c.sink_tiles];
     l = std::max(l, n);
@@ -697,6 +702,20 @@ BwdChunks bwd_chunks(int B, int H, int Hk, const Window& w) {
     c.counts[i] = cut ? ceil_div(longest[i], c.chunks[i]) : 1;
   }
   c.heads = B * Hk;
+  return c;
+}
+
+BwdCut bwd_cut(int B, int H, int Hk, const Window& w) {
+  const int tiles = ceil_div(w.Nk, BB), group = H / Hk;
+  BwdCut c;
+  static_cast<BwdChunks&>(c) = bwd_chunks(B, H, Hk, w);
+  for (int k = 0; k < 2; ++k) {
+    c.from[k] = c.to[k] = k ? c.sink_tiles : 0;
+    if (c.counts[k] == 1) continue;
+    c.to[k] = k ? tiles : c.sink_tiles;
+    while (tile_pairs(w, c.from[k], group) <= c.chunks[k]) ++c.from[k];  // (the longest tile stops both)
+    while (tile_pairs(w, c.to[k] - 1, group) <= c.chunks[k]) --c.to[k];
+  }
   return c;
 }
 

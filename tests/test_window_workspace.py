@@ -39,3 +39,10 @@ SHAPES = [
 def test_fp32_shares_are_those_of_the_tiles_in_chunks(lib, shape):
     D = shape[5]
     assert shares(lib, 0, *shape) <= 3 * 2 * 444 * 64 * D * 4
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_bf16_shares_are_those_of_the_tiles_in_parts(lib, shape):
+    # parts of at least eight pairs and at least an SM's share (148 in all), two gradients of 128 rows
+    D = shape[5]
+    assert shares(lib, 1, *shape) <= 3 * 148 * 2 * 128 * D * 4
