@@ -4,14 +4,20 @@ to the attention's, back to the projection's gradient, and token by token.
     qkv [B, N, H + 2 Hk, D] -> qk_norm_rope -> window_attn_fwd -> out [B, H, N, D]
 
 `forward` and `backward` are one training step; with keep8 what lies between
-them is held in 8 bits (the rows of q and k before their norm, v, and the
-output), q and k being recomputed from their rows.  `Stream` is the cached
-form.  This module only strings the calls together and moves v between the
-projection's token-major layout and the attention's head-major one.
+them is held in 8 bits (the rows of q and k before their norm, and v), and the
+backward first repeats the forward from them: its gradients are those of the
+step on the values that the rows stand for.  (The output and lse of the first
+forward do not belong to those values.  With them the rows of P would not sum to
+1 nor those of dS to 0, and dQ, a small difference of large sums where the keys
+share a common part, would be off several times as far: by 12 % in place of 3 %
+for keys with a common part of three times their spread and one outlying
+column.)  `Stream` is the cached form.  This module only strings the calls
+together and moves v between the projection's token-major layout and the
+attention's head-major one.
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional, Union
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -39,8 +45,8 @@ class Saved(NamedTuple):
     q: Optional[torch.Tensor]          # None with keep8: recomputed
     k: Optional[torch.Tensor]
     v: Union[torch.Tensor, Act8]       # [B, Hk, N, D]
-    out: Union[torch.Tensor, Act8]
-    lse: torch.Tensor
+    out: Union[torch.Tensor, Tuple[()]]  # () and None with keep8: recomputed
+    lse: Optional[torch.Tensor]
     wq: Optional[torch.Tensor]
     wk: Optional[torch.Tensor]
     plan: ops.RopePlan
@@ -67,9 +73,9 @@ def forward(qkv: torch.Tensor, heads: int, wq: Optional[torch.Tensor], wk: Optio
         q, k, q8, k8 = ops.qk_norm_rope(xq, xk, wq, wk, plan, eps, save8=True)
     else:
         q, k = ops.qk_norm_rope(xq, xk, wq, wk, plan, eps)
-    out, lse = ops.window_attn_fwd(q, k, v, mask.left, mask.right, mask.sink, scale=scale)
+    out, lse = ops.window_attn_fwd(q, k, v, mask.left, mask.right, mask.sink, scale=scale, want_lse=not keep8)
     if keep8:
-        saved = Saved(q8, k8, None, None, ops.pack8(v), ops.pack8(out), lse, wq, wk, plan, eps, mask, scale)
+        saved = Saved(q8, k8, None, None, ops.pack8(v), (), None, wq, wk, plan, eps, mask, scale)
     else:
         saved = Saved(xq, xk, q, k, v, out, lse, wq, wk, plan, eps, mask, scale)
     return out, saved
@@ -77,13 +83,14 @@ def forward(qkv: torch.Tensor, heads: int, wq: Optional[torch.Tensor], wk: Optio
 
 def backward(dout: torch.Tensor, s: Saved):
     """(dqkv [B, N, H + 2 Hk, D], dwq, dwk) for dout [B, H, N, D]."""
-    q, k, v, out = s.q, s.k, s.v, s.out
+    q, k, v, out, lse = s.q, s.k, s.v, s.out, s.lse
     if q is None:
         q, k = ops.qk_norm_rope(s.xq, s.xk, s.wq, s.wk, s.plan, s.eps, dtype=dout.dtype)
-        v, out = ops.unpack8(s.v, dout.dtype), ops.unpack8(s.out, dout.dtype)
+        v = ops.unpack8(s.v, dout.dtype)
+        out, lse = ops.window_attn_fwd(q, k, v, s.mask.left, s.mask.right, s.mask.sink, scale=s.scale)
     B, H, N, D = q.shape
     Hk = k.shape[1]
-    dq, dk, dv = ops.window_attn_bwd(q, k, v, out, dout, s.lse, s.mask.left, s.mask.right, s.mask.sink,
+    dq, dk, dv = ops.window_attn_bwd(q, k, v, out, dout, lse, s.mask.left, s.mask.right, s.mask.sink,
                                      scale=s.scale)
     dqkv = torch.empty(B, N, H + 2 * Hk, D, device=dout.device, dtype=dout.dtype)
     dxq, dxk, dxv = _split(dqkv, H)
