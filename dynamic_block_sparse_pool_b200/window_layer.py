@@ -125,29 +125,27 @@ class Stream:
         self.length = 0
 
     def step(self, qkv: torch.Tensor, pos: torch.Tensor) -> torch.Tensor:
-        B, Hk, capacity, D = self.k.shape
-        want = (B, self.heads + 2 * Hk, D)
-        if qkv.dim() != 4 or (qkv.shape[0], *qkv.shape[2:]) != want or qkv.dtype != self.k.dtype \
-                or qkv.device != self.k.device:
-            raise ValueError(f"a step of this stream takes {want[0]} x n x {want[1]} x {D} values of {self.k.dtype} "
-                             f"on {self.k.device}")
-        n = qkv.shape[1]
-        if self.length + n > capacity:
-            raise ValueError(f"{self.length} + {n} tokens exceed the capacity of {capacity}")
+        cache, n = self.k, qkv.shape[1] if qkv.dim() == 4 else -1
+        if n < 0 or qkv.shape != (cache.shape[0], n, self.heads + 2 * cache.shape[1], cache.shape[3]) \
+                or qkv.dtype != cache.dtype or qkv.device != cache.device:
+            raise ValueError(f"a step of this stream takes [{cache.shape[0]}, n, {self.heads + 2 * cache.shape[1]}, "
+                             f"{cache.shape[3]}] of {cache.dtype} on {cache.device}")
+        if self.length + n > cache.shape[2]:
+            raise ValueError(f"{self.length} + {n} tokens exceed the capacity of {cache.shape[2]}")
         xq, xk, xv = _split(qkv, self.heads)
         q, k = ops.qk_norm_rope(xq, xk, self.wq, self.wk, self.plan.at(pos), self.eps)
         if n == 0:
             return q
         # rows past `lens` are not read: they count once every piece is on its way
-        self.k[:, :, self.length:self.length + n] = k
+        cache[:, :, self.length:self.length + n] = k
         self.v[:, :, self.length:self.length + n] = xv.transpose(1, 2)
         outs, at = [], 0
         try:
-            for piece in q.split(_MOST_NEW, 2):
+            for piece in (q,) if n <= _MOST_NEW else (x.contiguous() for x in q.split(_MOST_NEW, 2)):
                 self.lens += piece.shape[2]
                 at += piece.shape[2]
-                outs.append(ops.window_attn_decode(piece.contiguous(), self.k, self.v, self.lens, self.mask.left,
-                                                   self.mask.sink, self.scale))
+                outs.append(ops.window_attn_decode(piece, cache, self.v, self.lens, self.mask.left, self.mask.sink,
+                                                   self.scale))
             out = outs[0] if len(outs) == 1 else torch.cat(outs, 2)
         except BaseException:
             self.lens -= at
