@@ -274,10 +274,13 @@ __device__ __forceinline__ void read_slot(const uint4* slot, Raw<float>& r, int)
   r.v = slot[0];
   r.w = slot[kThreads];
 }
+// (the scale lies in the first thread's slot: it reads it and hands it on.  Read by
+// all from that slot it takes a fence on either side, before and after, since the
+// next copy into the slot is the first thread's: 2 % slower in bf16.)
 __device__ __forceinline__ void read_slot(const uint4* slot, Raw<int8_t>& r, int sub) {
-  __syncwarp();  // the scale is another thread's copy, and that thread has waited for it
   r.v = *reinterpret_cast<const uint2*>(slot);
-  r.scale = *reinterpret_cast<const float*>(reinterpret_cast<const uint32_t*>(slot - sub) + 2);
+  r.scale = __shfl_sync(0xffffffffu, *reinterpret_cast<const float*>(reinterpret_cast<const uint32_t*>(slot) + 2),
+                        (threadIdx.x & 31) - sub);
 }
 
 // Steps of the backward whose loads are in flight: enough bytes for HBM's
@@ -355,9 +358,6 @@ qk_norm_rope_bwd_kernel(const BwdArgs<TX, TG> a) {
     turn.load(a.rope, b, n, sub, a.err);
     turn.reverse();
     for (int h = ha + slot; h - slot < hz; h += RPW) {
-      // (codes: the copy that starts now goes into the slot whose scale the row's
-      // other threads read a step ago; shuffles do not order those reads before it)
-      if constexpr (sizeof(TX) == 1) __syncwarp();
       fetch_step();
       copy_wait<kDepth - 1>();
       const uint4* from = ring + (rs % kDepth) * (SLOTS * kThreads) + threadIdx.x;
