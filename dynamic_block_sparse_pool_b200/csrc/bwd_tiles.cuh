@@ -1,5 +1,5 @@
 // Tiles and products of the tensor-core backward passes: blocks of 128 rows,
-// bf16 operands, P and dS as two bf16 terms each.
+// bf16 operands, P and dS as one or two bf16 terms each.
 #pragma once
 
 #include "sm100.cuh"

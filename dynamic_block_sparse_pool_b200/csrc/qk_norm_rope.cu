@@ -25,11 +25,12 @@
 // and the forward can write those of x beside y, so a training step keeps a
 // byte per value where it kept two and reads less in the backward.
 //
-// Measured, D = 128, bf16, counted bytes (each value once): 118,800 tokens, 24 +
-// 24 heads: forward 469 us (6.2 TB/s), saving codes 646 (5.6), from codes 424
-// (5.2), backward 697 (6.3), from codes 740 (4.9); there 65 to 80 % of the issue
-// slots are taken.  75,600 tokens, 40 + 40 heads: forward 506 us (6.1).  D = 64,
-// 17,776 tokens, 48 + 48 heads: backward 120 us (5.5).
+// Measured, D = 128, bf16, counted bytes (each value once), L2 flushed between
+// calls: 118,800 tokens, 24 + 24 heads: forward 469 us (6.2 TB/s), saving codes 646
+// (5.6), from codes 424 (5.2), backward 697 (6.3), from codes 740 (4.9; 65 to 80 %
+// of the issue slots are taken); back to back the forward that saves codes and the
+// backward from them take 1,512 us together.  75,600 tokens, 40 + 40 heads: forward
+// 506 us (6.1).  D = 64, 17,776 tokens, 48 + 48 heads: backward 120 us (5.5).
 #include <algorithm>
 
 #include "norm_rope.cuh"

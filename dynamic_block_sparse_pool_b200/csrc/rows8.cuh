@@ -5,12 +5,13 @@
 // 8-bit rows: one fp32 scale = amax / 127 for each row and int8 codes =
 // round-half-even(x * (127 / amax)), every operation rounded to fp32, so a
 // program that repeats the three operations gets the same codes.  A code is
-// off by at most half a step: amax / 254 (against amax / 16 next to amax for
-// e4m3, whose smaller steps near zero win only for rows with far outliers).
+// off by at most half a step: amax / 254 (against amax / 28 next to amax for
+// e4m3 with amax at its largest value, 448, where a step is 32; its smaller steps
+// near zero win only for rows with far outliers).
 // amax is taken on the magnitude bits, which order NaN above infinity above
 // every finite value: a row with a non-finite value gets scale NaN and comes
-// back as NaN throughout.  A row whose amax is below 2^-119 (127 / amax
-// would overflow) is held as zeros.
+// back as NaN throughout.  A row whose amax is below 2^-119 is held as zeros:
+// its scale, amax / 127, would not be a normal fp32 number.
 #pragma once
 
 #include "common.cuh"

@@ -41,7 +41,8 @@
 // (4 products), and the pass some 640 beside exp2 for waiting, reading tensor
 // memory and handing over, which its two warps per scheduler, in phase, do not
 // cover.  A delay of half the warps by a third of a pass, so that one half computes
-// while the other reads, costs 5 %.  48 heads: 4.9 ms in all (575 TFLOP/s).
+// while the other reads, costs 5 %.  48 heads: 4.9 ms in all (575 TFLOP/s) with L2
+// flushed between calls, 5.5 ms (515) back to back under the power cap.
 // 8,192 tokens, 16 query heads on 4, D = 128, causal over 2,048, four sinks: dq
 // 229 us, dkdv 270 (357 with the sinks' tile uncut and last, 376 with dP ahead
 // of the gradients), 0.47 ms in all (640 TFLOP/s); causal without a window

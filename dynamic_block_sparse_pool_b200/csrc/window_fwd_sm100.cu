@@ -44,7 +44,8 @@
 //
 // Measured, D = 128: 75,600 tokens, 40 heads, 7,200 to either side 21.1 ms (1,005
 // TFLOP/s), 2 x 8,192 tokens, 32 heads on 8, causal over 2,048 with four sinks
-// 0.51 ms (945).  The tensor cores work 55 % of the cycles: an MMA issuer takes
+// 0.51 ms (945) with L2 flushed between calls, 0.57 (841) back to back under the
+// power cap.  The tensor cores work 55 % of the cycles: an MMA issuer takes
 // as long as its MMAs, and the softmax of a tile (exp2, a quarter of the issue
 // slots) hides behind the other tile's MMAs only in part.
 #include "sm100.cuh"
